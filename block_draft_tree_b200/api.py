@@ -32,7 +32,8 @@ EXPORTED = ("ddt_status_string", "ddt_mask_words", "ddt_topk_workspace_size", "d
             "ddt_kv_commit", "ddt_lm_head_max_rows", "ddt_lm_head_walk_workspace_size",
             "ddt_lm_head_walk", "ddt_tree_attn_plan", "ddt_debug_set_wait_limit",
             "ddt_topk_noalloc", "ddt_tree_walk_resolve_mode", "ddt_plan_budget",
-            "ddt_debug_set_attn_kernel")
+            "ddt_debug_set_attn_kernel", "ddt_kv_append_q8", "ddt_kv_commit_q8",
+            "ddt_kv_read_q8", "ddt_tree_attn_q8_workspace_size", "ddt_tree_attn_q8")
 
 # ddt_tree_walk's modes
 WALK_ALL_ROWS, WALK_LAZY, WALK_AUTO = 0, 1, 2
@@ -63,6 +64,50 @@ class LmHeadWalkArgs(ctypes.Structure):
                 ("acc_nodes", ctypes.c_void_p), ("acc_tok", ctypes.c_void_p),
                 ("bonus", ctypes.c_void_p), ("row_token", ctypes.c_void_p),
                 ("dev_status", ctypes.c_void_p)]
+
+
+class Q8Cache(ctypes.Structure):
+    """Mirror of ``ddt_q8_cache`` (field order and types as in ddt.h)."""
+    _fields_ = [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+                ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("block", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("t_max", ctypes.c_int64), ("hkv", ctypes.c_int),
+                ("d", ctypes.c_int)]
+
+
+class KVAppendQ8Args(ctypes.Structure):
+    """Mirror of ``ddt_kv_append_q8_args`` (field order and types as in ddt.h)."""
+    _fields_ = [("cache", Q8Cache), ("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p),
+                ("n_new", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p),
+                ("ctx_len_out", ctypes.c_void_p), ("batch", ctypes.c_int),
+                ("n_max", ctypes.c_int), ("dev_status", ctypes.c_void_p)]
+
+
+class KVCommitQ8Args(ctypes.Structure):
+    """Mirror of ``ddt_kv_commit_q8_args`` (field order and types as in ddt.h)."""
+    _fields_ = [("cache", Q8Cache), ("k_tree", ctypes.c_void_p), ("v_tree", ctypes.c_void_p),
+                ("acc_len", ctypes.c_void_p), ("acc_nodes", ctypes.c_void_p),
+                ("ctx_len", ctypes.c_void_p), ("ctx_len_out", ctypes.c_void_p),
+                ("batch", ctypes.c_int), ("n_max", ctypes.c_int), ("L", ctypes.c_int),
+                ("dev_status", ctypes.c_void_p)]
+
+
+class KVReadQ8Args(ctypes.Structure):
+    """Mirror of ``ddt_kv_read_q8_args`` (field order and types as in ddt.h)."""
+    _fields_ = [("cache", Q8Cache), ("ctx_len", ctypes.c_void_p), ("first", ctypes.c_void_p),
+                ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p), ("batch", ctypes.c_int),
+                ("n_max", ctypes.c_int), ("dev_status", ctypes.c_void_p)]
+
+
+class AttnQ8Args(ctypes.Structure):
+    """Mirror of ``ddt_attn_q8_args`` (field order and types as in ddt.h)."""
+    _fields_ = [("cache", Q8Cache), ("q", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p),
+                ("max_ctx", ctypes.c_int), ("k_tree", ctypes.c_void_p),
+                ("v_tree", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+                ("n_nodes", ctypes.c_void_p), ("batch", ctypes.c_int), ("n_max", ctypes.c_int),
+                ("hq", ctypes.c_int), ("scale", ctypes.c_float), ("out", ctypes.c_void_p),
+                ("lse_out", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
 
 
 class DDTError(RuntimeError):
@@ -142,6 +187,15 @@ def load_library():
         lib.ddt_lm_head_walk.argtypes = [ctypes.POINTER(LmHeadWalkArgs), vp, sz, vp]
         lib.ddt_kv_commit.restype = i32
         lib.ddt_kv_commit.argtypes = [ctypes.POINTER(KVCommitArgs), vp]
+        for name, args in (("ddt_kv_append_q8", KVAppendQ8Args),
+                           ("ddt_kv_commit_q8", KVCommitQ8Args),
+                           ("ddt_kv_read_q8", KVReadQ8Args)):
+            getattr(lib, name).restype = i32
+            getattr(lib, name).argtypes = [ctypes.POINTER(args), vp]
+        lib.ddt_tree_attn_q8_workspace_size.restype = sz
+        lib.ddt_tree_attn_q8_workspace_size.argtypes = [ctypes.POINTER(AttnQ8Args)]
+        lib.ddt_tree_attn_q8.restype = i32
+        lib.ddt_tree_attn_q8.argtypes = [ctypes.POINTER(AttnQ8Args), vp, sz, vp]
         u64 = ctypes.c_uint64
         lib.ddt_tree_walk_sample.restype = i32
         lib.ddt_tree_walk_sample.argtypes = [vp, i32, i32, i32, i32, i64, vp, vp, vp, vp, i32,
@@ -655,3 +709,227 @@ def lm_head_walk(hidden: torch.Tensor, weight: torch.Tensor, tok: torch.Tensor,
         rc = lib.ddt_lm_head_walk(ctypes.byref(a), _ptr(ws), nb, _stream(dev))
     _check(rc, "ddt_lm_head_walk")
     return res
+
+
+# ---------------------------------------------------------------------------
+# The 8-bit key/value cache: e4m3 codes (torch.float8_e4m3fn) in the layout of
+# the bf16 cache and int8 exponents, one per block of tokens and kv head; an
+# element's value is code * 2^exponent.
+
+Q8_BLOCKS = (16, 32, 64, 128)
+Q8_EXP_MIN, Q8_EXP_MAX = -48, 48
+
+
+def _q8_cache(fn: str, b: int, k_cache, v_cache, k_exp, v_exp, block: int, page_table) -> Q8Cache:
+    """Check the cache's tensors against each other and marshal them: codes
+    [b, t_max, hkv, d] with exponents [b, ceil(t_max / block), hkv], or with
+    ``page_table`` [b, max_pages] a pool [pages, page_size, hkv, d] with
+    exponents [pages, page_size / block, hkv]."""
+    if block not in Q8_BLOCKS:
+        raise DDTError("%s: block must be one of %s, got %r" % (fn, Q8_BLOCKS, block))
+    if k_cache.dim() != 4 or k_cache.dtype != torch.float8_e4m3fn or not k_cache.is_contiguous():
+        raise DDTError("%s: caches must be contiguous float8_e4m3fn [.., .., hkv, d], got %s %s"
+                       % (fn, k_cache.dtype, tuple(k_cache.shape)))
+    if v_cache.shape != k_cache.shape:
+        raise DDTError("%s: the V cache must have the K cache's shape" % fn)
+    _check_types(fn, (v_cache, torch.float8_e4m3fn), (k_exp, torch.int8), (v_exp, torch.int8),
+                 (page_table, torch.int32))
+    n0, n1, hkv, d = k_cache.shape
+    if page_table is None and n0 != b:
+        raise DDTError("%s: a dense cache must have %d sequences, got %d" % (fn, b, n0))
+    if page_table is not None:
+        if page_table.dim() != 2 or page_table.shape[0] != b:
+            raise DDTError("%s: page_table must be [%d, max_pages]" % (fn, b))
+        if n1 % block:
+            raise DDTError("%s: pages of %d tokens do not hold whole blocks of %d" % (fn, n1, block))
+    want = (n0, -(-n1 // block), hkv)
+    if tuple(k_exp.shape) != want or tuple(v_exp.shape) != want:
+        raise DDTError("%s: exponents must be %s, got %s and %s"
+                       % (fn, want, tuple(k_exp.shape), tuple(v_exp.shape)))
+    c = Q8Cache()
+    c.k_cache, c.v_cache = k_cache.data_ptr() or None, v_cache.data_ptr() or None
+    c.k_exp, c.v_exp = k_exp.data_ptr() or None, v_exp.data_ptr() or None
+    c.block, c.hkv, c.d = block, hkv, d
+    if page_table is None:
+        c.page_table, c.page_size, c.max_pages, c.num_pages, c.t_max = None, 0, 0, 0, n1
+    else:
+        c.page_table, c.page_size, c.max_pages = page_table.data_ptr(), n1, page_table.shape[1]
+        c.num_pages, c.t_max = n0, 0
+    return c
+
+
+def _check_rows_q8(fn: str, k, v, k_cache):
+    """Raise unless k and v are contiguous bf16 [batch, n, hkv, d] rows for the cache."""
+    if k.dim() != 4 or k_cache.dim() != 4 or k.shape[2:] != k_cache.shape[2:]:
+        raise DDTError("%s: rows must be [batch, n, %s], got %s"
+                       % (fn, ", ".join(str(x) for x in k_cache.shape[2:]), tuple(k.shape)))
+    if v.shape != k.shape:
+        raise DDTError("%s: the V rows must have the K rows' shape" % fn)
+    _check_types(fn, (k, torch.bfloat16), (v, torch.bfloat16))
+
+
+def _check_vectors(fn: str, b: int, **named):
+    """Raise unless every given tensor is a contiguous int32 [b]."""
+    for name, t in named.items():
+        if t is not None and (tuple(t.shape) != (b,) or t.dtype != torch.int32
+                              or not t.is_contiguous()):
+            raise DDTError("%s: %s must be a contiguous int32 [%d], got %s %s"
+                           % (fn, name, b, t.dtype, tuple(t.shape)))
+
+
+def kv_append_q8(k_new: torch.Tensor, v_new: torch.Tensor, ctx_len: torch.Tensor,
+                 k_cache: torch.Tensor, v_cache: torch.Tensor, k_exp: torch.Tensor,
+                 v_exp: torch.Tensor, block: int = 16, n_new: Optional[torch.Tensor] = None,
+                 page_table: Optional[torch.Tensor] = None, advance: bool = True,
+                 dev_status: Optional[torch.Tensor] = None):
+    """``ddt_kv_append_q8``: quantise rows i < n_new[b] (all when None) of the
+    bf16 K/V [batch, n_max, hkv, d] into the 8-bit cache at positions
+    ctx_len[b] + i, and (``advance``) add n_new to ``ctx_len`` in place.
+    ``k_cache`` / ``v_cache`` float8_e4m3fn, dense [batch, t_max, hkv, d] or a
+    pool [pages, page_size, hkv, d] with ``page_table`` [batch, max_pages];
+    ``k_exp`` / ``v_exp`` int8 [.., ceil(tokens / block), hkv]."""
+    lib = load_library()
+    fn = "kv_append_q8"
+    _check_rows_q8(fn, k_new, v_new, k_cache)
+    b, n_max = k_new.shape[:2]
+    _check_vectors(fn, b, ctx_len=ctx_len, n_new=n_new)
+    _check_types(fn, (dev_status, torch.int32))
+    a = KVAppendQ8Args()
+    a.cache = _q8_cache(fn, b, k_cache, v_cache, k_exp, v_exp, block, page_table)
+    dev = _need_cuda(k_new, v_new, ctx_len, k_cache, v_cache, k_exp, v_exp, n_new, page_table,
+                     dev_status)
+    a.k_new, a.v_new = k_new.data_ptr() or None, v_new.data_ptr() or None
+    a.n_new = None if n_new is None else n_new.data_ptr()
+    a.ctx_len = ctx_len.data_ptr()
+    a.ctx_len_out = ctx_len.data_ptr() if advance else None
+    a.batch, a.n_max = b, n_max
+    a.dev_status = None if dev_status is None else dev_status.data_ptr()
+    with torch.cuda.device(dev):
+        rc = lib.ddt_kv_append_q8(ctypes.byref(a), _stream(dev))
+    _check(rc, "ddt_kv_append_q8")
+
+
+def kv_commit_q8(k_tree: torch.Tensor, v_tree: torch.Tensor, acc_len: torch.Tensor,
+                 acc_nodes: torch.Tensor, ctx_len: torch.Tensor, k_cache: torch.Tensor,
+                 v_cache: torch.Tensor, k_exp: torch.Tensor, v_exp: torch.Tensor,
+                 block: int = 16, page_table: Optional[torch.Tensor] = None,
+                 advance: bool = True, dev_status: Optional[torch.Tensor] = None):
+    """``ddt_kv_commit_q8``: :func:`kv_commit` into the 8-bit cache (described
+    at :func:`kv_append_q8`): the root's and the accepted rows of the tree K/V
+    are quantised behind the context, and (``advance``) ``ctx_len`` grows in
+    place by acc_len + 1."""
+    lib = load_library()
+    fn = "kv_commit_q8"
+    _check_rows_q8(fn, k_tree, v_tree, k_cache)
+    b, n_max = k_tree.shape[:2]
+    _check_vectors(fn, b, acc_len=acc_len, ctx_len=ctx_len)
+    if acc_nodes.dim() != 2 or acc_nodes.shape[0] != b:
+        raise DDTError("%s: acc_nodes must be [%d, L]" % (fn, b))
+    _check_types(fn, (acc_nodes, torch.int32), (dev_status, torch.int32))
+    a = KVCommitQ8Args()
+    a.cache = _q8_cache(fn, b, k_cache, v_cache, k_exp, v_exp, block, page_table)
+    dev = _need_cuda(k_tree, v_tree, acc_len, acc_nodes, ctx_len, k_cache, v_cache, k_exp, v_exp,
+                     page_table, dev_status)
+    a.k_tree, a.v_tree = k_tree.data_ptr(), v_tree.data_ptr()
+    a.acc_len, a.acc_nodes = acc_len.data_ptr(), acc_nodes.data_ptr() or None
+    a.ctx_len = ctx_len.data_ptr()
+    a.ctx_len_out = ctx_len.data_ptr() if advance else None
+    a.batch, a.n_max, a.L = b, n_max, acc_nodes.shape[1]
+    a.dev_status = None if dev_status is None else dev_status.data_ptr()
+    with torch.cuda.device(dev):
+        rc = lib.ddt_kv_commit_q8(ctypes.byref(a), _stream(dev))
+    _check(rc, "ddt_kv_commit_q8")
+
+
+def kv_read_q8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_exp: torch.Tensor,
+               v_exp: torch.Tensor, ctx_len: torch.Tensor, n_max: int, block: int = 16,
+               first: Optional[torch.Tensor] = None, page_table: Optional[torch.Tensor] = None,
+               dev_status: Optional[torch.Tensor] = None):
+    """``ddt_kv_read_q8``: positions first[b] + r (first None: 0), r < n_max, of
+    the 8-bit cache (described at :func:`kv_append_q8`) as bf16.  Returns (k, v)
+    [batch, n_max, hkv, d]; rows at or past ctx_len[b] are 0."""
+    lib = load_library()
+    fn = "kv_read_q8"
+    b = ctx_len.shape[0] if ctx_len.dim() == 1 else -1
+    _check_vectors(fn, b, ctx_len=ctx_len, first=first)
+    _check_types(fn, (dev_status, torch.int32))
+    if n_max < 0:
+        raise DDTError("%s: n_max must not be negative" % fn)
+    a = KVReadQ8Args()
+    a.cache = _q8_cache(fn, b, k_cache, v_cache, k_exp, v_exp, block, page_table)
+    dev = _need_cuda(k_cache, v_cache, k_exp, v_exp, ctx_len, first, page_table, dev_status)
+    hkv, d = k_cache.shape[2:]
+    k = torch.empty((b, n_max, hkv, d), dtype=torch.bfloat16, device=dev)
+    v = torch.empty_like(k)
+    a.ctx_len, a.first = ctx_len.data_ptr(), None if first is None else first.data_ptr()
+    a.k_out, a.v_out = k.data_ptr() or None, v.data_ptr() or None
+    a.batch, a.n_max = b, n_max
+    a.dev_status = None if dev_status is None else dev_status.data_ptr()
+    with torch.cuda.device(dev):
+        rc = lib.ddt_kv_read_q8(ctypes.byref(a), _stream(dev))
+    _check(rc, "ddt_kv_read_q8")
+    return k, v
+
+
+def _attn_q8_args(q, k_cache, v_cache, k_exp, v_exp, k_tree, v_tree, mask, n_nodes, ctx_len,
+                  max_ctx, block, scale, page_table, out, lse_out, dev_status) -> AttnQ8Args:
+    fn = "tree_attn_q8"
+    if q.dim() != 4:
+        raise DDTError("%s: q must be [batch, n_max, hq, d]" % fn)
+    b, n_max, hq, d = q.shape
+    _check_rows_q8(fn, k_tree, v_tree, k_cache)
+    if tuple(k_tree.shape[:2]) != (b, n_max) or k_tree.shape[3] != d:
+        raise DDTError("%s: tree K must be [%d, %d, hkv, %d], got %s"
+                       % (fn, b, n_max, d, tuple(k_tree.shape)))
+    if tuple(mask.shape) != (b, n_max, mask_words(n_max)):
+        raise DDTError("%s: mask must be [%d, %d, %d], got %s"
+                       % (fn, b, n_max, mask_words(n_max), tuple(mask.shape)))
+    _check_types(fn, (q, torch.bfloat16), (mask, torch.int32), (dev_status, torch.int32))
+    _check_vectors(fn, b, n_nodes=n_nodes, ctx_len=ctx_len)
+    a = AttnQ8Args()
+    a.cache = _q8_cache(fn, b, k_cache, v_cache, k_exp, v_exp, block, page_table)
+    a.q, a.ctx_len, a.max_ctx = q.data_ptr(), ctx_len.data_ptr(), int(max_ctx)
+    a.k_tree, a.v_tree = k_tree.data_ptr(), v_tree.data_ptr()
+    a.mask, a.n_nodes = mask.data_ptr(), n_nodes.data_ptr()
+    a.batch, a.n_max, a.hq = b, n_max, hq
+    a.scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    a.out = out.data_ptr()
+    a.lse_out = None if lse_out is None else lse_out.data_ptr()
+    a.dev_status = None if dev_status is None else dev_status.data_ptr()
+    return a
+
+
+def tree_attn_q8_workspace_size(q, k_cache, v_cache, k_exp, v_exp, k_tree, v_tree, mask, n_nodes,
+                                ctx_len, max_ctx, block=16, scale=None, page_table=None) -> int:
+    # the output pointer only has to be valid for the argument check: q stands in
+    a = _attn_q8_args(q, k_cache, v_cache, k_exp, v_exp, k_tree, v_tree, mask, n_nodes, ctx_len,
+                      max_ctx, block, scale, page_table, q, None, None)
+    with torch.cuda.device(q.device):
+        return int(load_library().ddt_tree_attn_q8_workspace_size(ctypes.byref(a)))
+
+
+def tree_attn_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 k_exp: torch.Tensor, v_exp: torch.Tensor, k_tree: torch.Tensor,
+                 v_tree: torch.Tensor, mask: torch.Tensor, n_nodes: torch.Tensor,
+                 ctx_len: torch.Tensor, max_ctx: int, block: int = 16,
+                 scale: Optional[float] = None, page_table: Optional[torch.Tensor] = None,
+                 want_lse: bool = False, dev_status: Optional[torch.Tensor] = None):
+    """``ddt_tree_attn_q8``: :func:`tree_attn` over the 8-bit cache (described
+    at :func:`kv_append_q8`); the tree rows' own K/V stay bf16.  An ordinary
+    decoding step is n_max = 1 with mask word 1.  Returns out bf16 [batch,
+    n_max, hq, d] (and lse f32 [batch, n_max, hq] when asked)."""
+    lib = load_library()
+    a = _attn_q8_args(q, k_cache, v_cache, k_exp, v_exp, k_tree, v_tree, mask, n_nodes, ctx_len,
+                      max_ctx, block, scale, page_table, q, None, dev_status)
+    dev = _need_cuda(q, k_cache, v_cache, k_exp, v_exp, k_tree, v_tree, mask, n_nodes, ctx_len,
+                     page_table, dev_status)
+    out = torch.empty_like(q)
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if want_lse else None
+    a.out, a.lse_out = out.data_ptr(), None if lse is None else lse.data_ptr()
+    with torch.cuda.device(dev):
+        nb = int(lib.ddt_tree_attn_q8_workspace_size(ctypes.byref(a)))
+        # scratch of this call alone: calls on other streams and captured graphs have their own
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+        rc = lib.ddt_tree_attn_q8(ctypes.byref(a), _ptr(ws), nb, _stream(dev))
+    _check(rc, "ddt_tree_attn_q8")
+    return (out, lse) if want_lse else out

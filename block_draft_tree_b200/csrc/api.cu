@@ -469,4 +469,109 @@ ddt_status ddt_kv_commit(const ddt_kv_commit_args* a, cudaStream_t stream) {
   return launch_kv_commit(a, stream);
 }
 
+// ---------------------------------------------------------------- 8-bit cache
+static ddt_status check_q8(const ddt_q8_cache* c) {
+  if (c->hkv < 1) return DDT_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return DDT_ERR_UNSUPPORTED;
+  if (c->hkv > 65535) return DDT_ERR_UNSUPPORTED;
+  if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) return DDT_ERR_UNSUPPORTED;
+  return DDT_OK;
+}
+
+// The cache's memory, for a call that reaches it.
+static ddt_status check_q8_memory(const ddt_q8_cache* c) {
+  if (!c->k_cache || !c->v_cache || !c->k_exp || !c->v_exp) return DDT_ERR_INVALID_ARG;
+  if (!aligned16(c->k_cache) || !aligned16(c->v_cache)) return DDT_ERR_INVALID_ARG;
+  if (c->page_table) {
+    if (c->page_size < 1 || c->max_pages < 1 || c->num_pages < 1) return DDT_ERR_INVALID_ARG;
+    if (c->page_size % c->block != 0) return DDT_ERR_UNSUPPORTED;
+  } else if (c->t_max < 1) {
+    return DDT_ERR_INVALID_ARG;
+  }
+  return DDT_OK;
+}
+
+ddt_status ddt_kv_append_q8(const ddt_kv_append_q8_args* a, cudaStream_t stream) {
+  const NvtxRange nvtx("ddt_kv_append_q8");
+  if (!a) return DDT_ERR_INVALID_ARG;
+  if (a->batch < 0 || a->n_max < 0) return DDT_ERR_INVALID_ARG;
+  if (a->batch > 65535) return DDT_ERR_UNSUPPORTED;
+  ddt_status st = check_q8(&a->cache);
+  if (st != DDT_OK) return st;
+  if (a->batch == 0) return DDT_OK;
+  if (!a->ctx_len || (a->n_max > 0 && (!a->k_new || !a->v_new))) return DDT_ERR_INVALID_ARG;
+  if (!aligned16(a->k_new) || !aligned16(a->v_new)) return DDT_ERR_INVALID_ARG;
+  st = check_q8_memory(&a->cache);
+  if (st != DDT_OK) return st;
+  return launch_kv_append_q8(a, stream);
+}
+
+ddt_status ddt_kv_commit_q8(const ddt_kv_commit_q8_args* a, cudaStream_t stream) {
+  const NvtxRange nvtx("ddt_kv_commit_q8");
+  if (!a) return DDT_ERR_INVALID_ARG;
+  if (a->batch < 0 || a->n_max < 1 || a->L < 0) return DDT_ERR_INVALID_ARG;
+  if (a->batch > 65535 || a->L > DDT_TREE_L_MAX) return DDT_ERR_UNSUPPORTED;
+  ddt_status st = check_q8(&a->cache);
+  if (st != DDT_OK) return st;
+  if (a->batch == 0) return DDT_OK;
+  if (!a->k_tree || !a->v_tree || !a->acc_len || !a->ctx_len || (a->L > 0 && !a->acc_nodes))
+    return DDT_ERR_INVALID_ARG;
+  if (!aligned16(a->k_tree) || !aligned16(a->v_tree)) return DDT_ERR_INVALID_ARG;
+  st = check_q8_memory(&a->cache);
+  if (st != DDT_OK) return st;
+  return launch_kv_commit_q8(a, stream);
+}
+
+ddt_status ddt_kv_read_q8(const ddt_kv_read_q8_args* a, cudaStream_t stream) {
+  const NvtxRange nvtx("ddt_kv_read_q8");
+  if (!a) return DDT_ERR_INVALID_ARG;
+  if (a->batch < 0 || a->n_max < 0) return DDT_ERR_INVALID_ARG;
+  if (a->batch > 65535) return DDT_ERR_UNSUPPORTED;
+  ddt_status st = check_q8(&a->cache);
+  if (st != DDT_OK) return st;
+  if (a->batch == 0 || a->n_max == 0) return DDT_OK;
+  if (!a->ctx_len || !a->k_out || !a->v_out) return DDT_ERR_INVALID_ARG;
+  if (!aligned16(a->k_out) || !aligned16(a->v_out)) return DDT_ERR_INVALID_ARG;
+  st = check_q8_memory(&a->cache);
+  if (st != DDT_OK) return st;
+  return launch_kv_read_q8(a, stream);
+}
+
+static ddt_status check_attn_q8(const ddt_attn_q8_args* a) {
+  if (!a) return DDT_ERR_INVALID_ARG;
+  if (a->batch < 0 || a->n_max < 1 || a->hq < 1 || a->max_ctx < 0) return DDT_ERR_INVALID_ARG;
+  ddt_status st = check_q8(&a->cache);
+  if (st != DDT_OK) return st;
+  if (a->hq % a->cache.hkv != 0) return DDT_ERR_INVALID_ARG;
+  if (a->n_max > DDT_TREE_B_MAX + 1 || (int64_t)a->batch * a->cache.hkv > 65535 || a->hq > 65535)
+    return DDT_ERR_UNSUPPORTED;
+  if (!(a->scale > 0.f) || !(a->scale < INFINITY)) return DDT_ERR_INVALID_ARG;
+  if (a->batch == 0) return DDT_OK;
+  if (!a->q || !a->k_tree || !a->v_tree || !a->mask || !a->n_nodes || !a->ctx_len || !a->out)
+    return DDT_ERR_INVALID_ARG;
+  if (!aligned16(a->q) || !aligned16(a->k_tree) || !aligned16(a->v_tree) || !aligned16(a->out))
+    return DDT_ERR_INVALID_ARG;
+  if (a->max_ctx > 0) {
+    st = check_q8_memory(&a->cache);
+    if (st != DDT_OK) return st;
+    const int64_t room = a->cache.page_table ? (int64_t)a->cache.max_pages * a->cache.page_size : a->cache.t_max;
+    if (room < a->max_ctx) return DDT_ERR_INVALID_ARG;
+  }
+  return DDT_OK;
+}
+
+size_t ddt_tree_attn_q8_workspace_size(const ddt_attn_q8_args* a) {
+  if (check_attn_q8(a) != DDT_OK) return 0;
+  return attn_q8_workspace_size(a);
+}
+
+ddt_status ddt_tree_attn_q8(const ddt_attn_q8_args* a, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  const NvtxRange nvtx("ddt_tree_attn_q8");
+  const ddt_status st = check_attn_q8(a);
+  if (st != DDT_OK) return st;
+  if (!ws_ok(workspace, workspace_bytes, attn_q8_workspace_size(a))) return DDT_ERR_WORKSPACE;
+  return launch_attn_q8(a, workspace, stream);
+}
+
 }  // extern "C"

@@ -94,6 +94,12 @@ ddt_status launch_plan_budget(const int32_t* tok, const int32_t* parent, const i
                               int32_t* budget, double* expected_tokens, int32_t* dev_status,
                               cudaStream_t stream);
 
+ddt_status launch_kv_append_q8(const ddt_kv_append_q8_args* a, cudaStream_t stream);
+ddt_status launch_kv_commit_q8(const ddt_kv_commit_q8_args* a, cudaStream_t stream);
+ddt_status launch_kv_read_q8(const ddt_kv_read_q8_args* a, cudaStream_t stream);
+size_t attn_q8_workspace_size(const ddt_attn_q8_args* a);
+ddt_status launch_attn_q8(const ddt_attn_q8_args* a, void* ws, cudaStream_t stream);
+
 struct AttnParams;
 size_t attn_workspace_size(const ddt_attn_args* a);
 ddt_status launch_attn(const ddt_attn_args* a, void* ws, size_t ws_bytes, cudaStream_t stream);

@@ -1,0 +1,89 @@
+// q8_common.cuh -- the 8-bit key/value cache: where a position's codes and
+// exponent lie, and the conversions between e4m3 codes, f16 and bf16.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace ddt {
+
+// Device view of ddt_q8_cache.
+struct Q8View {
+  uint8_t *kc, *vc;
+  int8_t *ke, *ve;
+  const int32_t* page_table;  // null: dense
+  int page_size, max_pages, num_pages;
+  int64_t t_max;
+  int hkv, d;
+  int block_log2;
+  int64_t blocks_per;         // exponent rows per sequence (dense) or page (paged)
+};
+
+// Cache row (token) of position t and its exponent row, or row -1 when the
+// position lies outside the cache.
+struct Q8Place {
+  int64_t row, blk;
+};
+__device__ __forceinline__ Q8Place q8_place(const Q8View& c, int b, int64_t t) {
+  Q8Place p{-1, -1};
+  if (t < 0) return p;
+  if (c.page_table == nullptr) {
+    if (t < c.t_max) {
+      p.row = (int64_t)b * c.t_max + t;
+      p.blk = (int64_t)b * c.blocks_per + (t >> c.block_log2);
+    }
+    return p;
+  }
+  if (t >= (int64_t)c.max_pages * c.page_size) return p;
+  const int pi = (int)((uint32_t)t / (uint32_t)c.page_size);
+  const int slot = (int)((uint32_t)t - (uint32_t)pi * (uint32_t)c.page_size);
+  const int pg = c.page_table[(int64_t)b * c.max_pages + pi];
+  if ((uint32_t)pg < (uint32_t)c.num_pages) {
+    p.row = (int64_t)pg * c.page_size + slot;
+    p.blk = (int64_t)pg * c.blocks_per + (slot >> c.block_log2);
+  }
+  return p;
+}
+
+__device__ __forceinline__ int q8_exp(int8_t e) {
+  return min(max((int)e, DDT_Q8_EXP_MIN), DDT_Q8_EXP_MAX);
+}
+// 2^e for |e| <= 126.
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// Two e4m3 codes (low byte first) -> two f16 (exact; NaN stays NaN).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+// Two floats -> two e4m3 codes (lo in the low byte), nearest-even, saturating.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// The larger magnitude bits of the finite ones among two packed bf16 and m.
+__device__ __forceinline__ uint32_t max_finite_bf16(uint32_t m, uint32_t w) {
+  const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
+  if (lo < 0x7F80u) m = max(m, lo);
+  if (hi < 0x7F80u) m = max(m, hi);
+  return m;
+}
+
+}  // namespace ddt

@@ -28,6 +28,11 @@ class VerifyRound:
     ``ddt_kv_commit``: the root's and the accepted rows' K/V join the bound
     cache and ``ctx_len`` advances in place.
 
+    With ``cache="q8"`` the bound K/V cache is the 8-bit one (``k_cache`` /
+    ``v_cache`` float8_e4m3fn with the int8 exponents ``k_exp`` / ``v_exp`` per
+    block of ``block`` tokens, as :func:`api.kv_append_q8` fills it): stage 3 is
+    ``ddt_tree_attn_q8`` and the commit ``ddt_kv_commit_q8``.
+
     With ``adaptive_budget`` (a dict of ``total``, ``cost_fixed``,
     ``cost_per_node``) stage 2 builds every sequence's tree with its largest
     budget, splits the batch's nodes with ``ddt_plan_budget`` under that cost
@@ -35,13 +40,19 @@ class VerifyRound:
     and ``out["expected_tokens"]`` hold the split.
     """
 
+    q8, block = False, 16  # the cache's form
+
     def __init__(self, *, batch: int, L: int, V: int, k: int, B_max: int, hq: int, hkv: int,
                  d: int, max_ctx: int, draft_dtype: torch.dtype = torch.bfloat16,
                  target_dtype: torch.dtype = torch.float32, inv_temperature: float = 1.0,
                  paged: bool = False, page_size: int = 64, max_pages: int = 0,
                  decode: str = "greedy", sample_inv_temperature: float = 1.0, seed: int = 0,
                  commit: bool = False, walk_mode: int = api.WALK_AUTO,
-                 adaptive_budget: Optional[dict] = None, device: str = "cuda"):
+                 adaptive_budget: Optional[dict] = None, device: str = "cuda",
+                 cache: str = "bf16", block: int = 16):
+        if cache not in ("bf16", "q8"):
+            raise ValueError("cache must be 'bf16' or 'q8'")
+        self.q8, self.block = cache == "q8", int(block)
         if decode not in ("greedy", "sample", "lm_head"):
             raise ValueError("decode must be 'greedy', 'sample' or 'lm_head'")
         self.decode, self.commit, self.walk_mode = decode, commit, int(walk_mode)
@@ -87,53 +98,95 @@ class VerifyRound:
     # ------------------------------------------------------------------
     def bind(self, inputs: dict):
         """Bind device input tensors: draft [b,L,V], root [b], ctx_len [b],
-        q [b,n,hq,d], k_cache/v_cache, optional page_table, k_tree/v_tree
-        [b,n,hkv,d], target [b,n,V]; optional k_per_seq / budget [b]."""
+        q [b,n,hq,d], k_cache/v_cache (and k_exp/v_exp of an 8-bit cache),
+        optional page_table, k_tree/v_tree [b,n,hkv,d], target [b,n,V];
+        optional k_per_seq / budget [b]."""
         self._check_inputs(inputs)
         self.inputs = inputs
+        if self.q8:
+            self._bind_attn_q8(inputs)
+        else:
+            self._bind_attn(inputs)
+        if self.decode == "lm_head":
+            self._bind_lm_head(inputs)
+        if self.commit:
+            if self.q8:
+                self._bind_commit_q8(inputs)
+            else:
+                self._bind_commit(inputs)
+
+    def _attn_workspace(self, n: int):
+        if self.ws_attn is None or self.ws_attn.numel() < n:
+            self.ws_attn = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.dev)
+        self.ws_attn_n = n
+
+    def _bind_attn(self, inputs: dict):
         o = self.out
         a = api._attn_args(inputs["q"], inputs["k_cache"], inputs["v_cache"], inputs["k_tree"],
                            inputs["v_tree"], o["mask"], o["n_nodes"], inputs["ctx_len"],
                            self.max_ctx, 1.0 / math.sqrt(self.d), inputs.get("page_table"),
                            o["attn"], None, o["status"])
         self.attn_args = a
-        n = int(self.lib.ddt_tree_attn_workspace_size(ctypes.byref(a)))
-        if self.ws_attn is None or self.ws_attn.numel() < n:
-            self.ws_attn = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.dev)
-        self.ws_attn_n = n
-        if self.decode == "lm_head":
-            hid, head = inputs["hidden"], inputs["head"]
-            la = api.LmHeadWalkArgs()
-            la.hidden, la.weight = hid.data_ptr(), head.data_ptr()
-            la.K, la.V = hid.shape[-1], head.shape[0]
-            la.tok, la.parent = o["tok"].data_ptr(), o["parent"].data_ptr()
-            la.depth, la.n_nodes = o["depth"].data_ptr(), o["n_nodes"].data_ptr()
-            la.batch, la.n_max, la.L = self.batch, self.n_max, self.L
-            la.acc_len, la.acc_nodes = o["acc_len"].data_ptr(), o["acc_nodes"].data_ptr()
-            la.acc_tok, la.bonus = o["acc_tok"].data_ptr(), o["bonus"].data_ptr()
-            la.row_token, la.dev_status = None, o["status"].data_ptr()
-            self.lm_args = la
-            nl = int(self.lib.ddt_lm_head_walk_workspace_size(ctypes.byref(la)))
-            if self.ws_lm is None or self.ws_lm.numel() < nl:
-                self.ws_lm = torch.zeros(max(nl, 256), dtype=torch.uint8, device=self.dev)
-            self.ws_lm_n = nl
-        if self.commit:
-            ca = api.KVCommitArgs()
-            ca.k_tree, ca.v_tree = inputs["k_tree"].data_ptr(), inputs["v_tree"].data_ptr()
-            ca.acc_len, ca.acc_nodes = o["acc_len"].data_ptr(), o["acc_nodes"].data_ptr()
-            ca.ctx_len = inputs["ctx_len"].data_ptr()
-            ca.k_cache, ca.v_cache = inputs["k_cache"].data_ptr(), inputs["v_cache"].data_ptr()
-            pt = inputs.get("page_table")
-            if pt is None:
-                ca.page_table, ca.page_size, ca.max_pages, ca.num_pages = None, 0, 0, 0
-                ca.t_max = inputs["k_cache"].shape[1]
-            else:
-                ca.page_table, ca.page_size = pt.data_ptr(), self.page_size
-                ca.max_pages, ca.num_pages = pt.shape[1], inputs["k_cache"].shape[0]
-                ca.t_max = 0
-            ca.batch, ca.n_max, ca.hkv, ca.d, ca.L = self.batch, self.n_max, self.hkv, self.d, self.L
-            ca.dev_status = o["status"].data_ptr()
-            self.commit_args = ca
+        self._attn_workspace(int(self.lib.ddt_tree_attn_workspace_size(ctypes.byref(a))))
+
+    def _bind_attn_q8(self, inputs: dict):
+        x, o = inputs, self.out
+        a = api._attn_q8_args(x["q"], x["k_cache"], x["v_cache"], x["k_exp"], x["v_exp"],
+                              x["k_tree"], x["v_tree"], o["mask"], o["n_nodes"], x["ctx_len"],
+                              self.max_ctx, self.block, None, x.get("page_table"), o["attn"], None,
+                              o["status"])
+        self.attn_args = a
+        with torch.cuda.device(self.dev):
+            self._attn_workspace(int(self.lib.ddt_tree_attn_q8_workspace_size(ctypes.byref(a))))
+
+    def _bind_lm_head(self, inputs: dict):
+        o = self.out
+        hid, head = inputs["hidden"], inputs["head"]
+        la = api.LmHeadWalkArgs()
+        la.hidden, la.weight = hid.data_ptr(), head.data_ptr()
+        la.K, la.V = hid.shape[-1], head.shape[0]
+        la.tok, la.parent = o["tok"].data_ptr(), o["parent"].data_ptr()
+        la.depth, la.n_nodes = o["depth"].data_ptr(), o["n_nodes"].data_ptr()
+        la.batch, la.n_max, la.L = self.batch, self.n_max, self.L
+        la.acc_len, la.acc_nodes = o["acc_len"].data_ptr(), o["acc_nodes"].data_ptr()
+        la.acc_tok, la.bonus = o["acc_tok"].data_ptr(), o["bonus"].data_ptr()
+        la.row_token, la.dev_status = None, o["status"].data_ptr()
+        self.lm_args = la
+        nl = int(self.lib.ddt_lm_head_walk_workspace_size(ctypes.byref(la)))
+        if self.ws_lm is None or self.ws_lm.numel() < nl:
+            self.ws_lm = torch.zeros(max(nl, 256), dtype=torch.uint8, device=self.dev)
+        self.ws_lm_n = nl
+
+    def _bind_commit(self, inputs: dict):
+        o = self.out
+        ca = api.KVCommitArgs()
+        ca.k_tree, ca.v_tree = inputs["k_tree"].data_ptr(), inputs["v_tree"].data_ptr()
+        ca.acc_len, ca.acc_nodes = o["acc_len"].data_ptr(), o["acc_nodes"].data_ptr()
+        ca.ctx_len = inputs["ctx_len"].data_ptr()
+        ca.k_cache, ca.v_cache = inputs["k_cache"].data_ptr(), inputs["v_cache"].data_ptr()
+        pt = inputs.get("page_table")
+        if pt is None:
+            ca.page_table, ca.page_size, ca.max_pages, ca.num_pages = None, 0, 0, 0
+            ca.t_max = inputs["k_cache"].shape[1]
+        else:
+            ca.page_table, ca.page_size = pt.data_ptr(), self.page_size
+            ca.max_pages, ca.num_pages = pt.shape[1], inputs["k_cache"].shape[0]
+            ca.t_max = 0
+        ca.batch, ca.n_max, ca.hkv, ca.d, ca.L = self.batch, self.n_max, self.hkv, self.d, self.L
+        ca.dev_status = o["status"].data_ptr()
+        self.commit_args = ca
+
+    def _bind_commit_q8(self, inputs: dict):
+        x, o = inputs, self.out
+        ca = api.KVCommitQ8Args()
+        ca.cache = api._q8_cache("bind", self.batch, x["k_cache"], x["v_cache"], x["k_exp"],
+                                 x["v_exp"], self.block, x.get("page_table"))
+        ca.k_tree, ca.v_tree = x["k_tree"].data_ptr(), x["v_tree"].data_ptr()
+        ca.acc_len, ca.acc_nodes = o["acc_len"].data_ptr(), o["acc_nodes"].data_ptr()
+        ca.ctx_len = ca.ctx_len_out = x["ctx_len"].data_ptr()
+        ca.batch, ca.n_max, ca.L = self.batch, self.n_max, self.L
+        ca.dev_status = o["status"].data_ptr()
+        self.commit_args = ca
 
     def _check_inputs(self, x: dict):
         """Refuse inputs whose shapes, dtypes or layouts differ from this
@@ -164,12 +217,20 @@ class VerifyRound:
                             ("v_tree", (b, n, self.hkv, self.d))):
             if not need(name, shape, torch.bfloat16).is_contiguous():
                 raise api.DDTError("bind: %r must be contiguous" % name)
-        api._check_types("bind", (x.get("k_cache"), torch.bfloat16),
-                         (x.get("v_cache"), torch.bfloat16), (x.get("page_table"), torch.int32))
         pt = x.get("page_table")
-        api._check_kv_shapes("bind", b, n, self.d, x["k_tree"], x["v_tree"], x.get("k_cache"),
-                             x.get("v_cache"), pt,
-                             self.page_size if self.commit and pt is not None else None)
+        if self.q8:
+            for name in ("k_cache", "v_cache", "k_exp", "v_exp"):
+                if x.get(name) is None:
+                    raise api.DDTError("bind: input %r is missing" % name)
+            api._check_rows_q8("bind", x["k_tree"], x["v_tree"], x["k_cache"])
+            api._q8_cache("bind", b, x["k_cache"], x["v_cache"], x["k_exp"], x["v_exp"],
+                          self.block, pt)
+        else:
+            api._check_types("bind", (x.get("k_cache"), torch.bfloat16),
+                             (x.get("v_cache"), torch.bfloat16), (pt, torch.int32))
+            api._check_kv_shapes("bind", b, n, self.d, x["k_tree"], x["v_tree"], x.get("k_cache"),
+                                 x.get("v_cache"), pt,
+                                 self.page_size if self.commit and pt is not None else None)
         if self.decode == "lm_head":
             hid, head = x.get("hidden"), x.get("head")
             if hid is None or head is None:
@@ -224,8 +285,9 @@ class VerifyRound:
                 api._check(rc, "ddt_plan_budget")
                 build(o["budget"])
         elif i == 2:
-            rc = lib.ddt_tree_attn(ctypes.byref(self.attn_args), P(self.ws_attn), self.ws_attn_n, s)
-            api._check(rc, "ddt_tree_attn")
+            name = "ddt_tree_attn_q8" if self.q8 else "ddt_tree_attn"
+            rc = getattr(lib, name)(ctypes.byref(self.attn_args), P(self.ws_attn), self.ws_attn_n, s)
+            api._check(rc, name)
         elif i == 3:
             if self.decode == "greedy":
                 rc = lib.ddt_tree_walk(P(x["target"]), self.target_code, self.batch, self.n_max,
@@ -249,8 +311,9 @@ class VerifyRound:
                                           s)
                 api._check(rc, "ddt_lm_head_walk")
         elif i == 4 and self.commit:
-            rc = lib.ddt_kv_commit(ctypes.byref(self.commit_args), s)
-            api._check(rc, "ddt_kv_commit")
+            name = "ddt_kv_commit_q8" if self.q8 else "ddt_kv_commit"
+            rc = getattr(lib, name)(ctypes.byref(self.commit_args), s)
+            api._check(rc, name)
         else:
             raise ValueError("no stage %d in this round" % i)
 

@@ -22,6 +22,10 @@
  *                      committed context for the next round.
  *   ddt_plan_budget    splits a batch's node budget between its sequences
  *                      (between a first and a second ddt_build_tree).
+ *   ddt_kv_append_q8, ddt_kv_commit_q8, ddt_kv_read_q8, ddt_tree_attn_q8
+ *                      the same attention and commit over a key/value cache
+ *                      held in 8 bits, with the calls that fill it and read
+ *                      it back.
  *
  * Conventions shared by every entry point:
  *   - Every tensor pointer is a DEVICE pointer owned by the caller.  The
@@ -488,6 +492,151 @@ ddt_status ddt_tree_walk_sample(const void* logits, ddt_dtype dtype, int batch, 
                                 uint64_t* step_counter, int32_t* acc_len, int32_t* acc_nodes,
                                 int32_t* acc_tok, int32_t* bonus, void* workspace,
                                 size_t workspace_bytes, int32_t* dev_status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit key/value cache.
+ *
+ * Codes: e4m3 (1 sign, 4 exponent, 3 fraction bits; no infinity, S.1111.111
+ * is NaN), one byte per element in the layout of the bf16 cache.  Scales: one
+ * int8 exponent e for every block of `block` tokens of every kv head, K and V
+ * apart; an element's value is code * 2^e.  Exponents lie in
+ * [DDT_Q8_EXP_MIN, DDT_Q8_EXP_MAX]; a stored exponent outside is read as the
+ * nearer end.  A power of two scales a code without rounding it, so a value
+ * is exactly a bf16 number and a block whose scale grows keeps its older
+ * codes exactly unless they become e4m3 subnormals.
+ *
+ *   dense  (page_table == NULL): codes [batch][t_max][hkv][d], exponents
+ *          [batch][ceil(t_max / block)][hkv];
+ *   paged: codes [num_pages][page_size][hkv][d], exponents
+ *          [num_pages][page_size / block][hkv]; context position t of
+ *          sequence b lives in page page_table[b*max_pages + t/page_size].
+ * Limits: d in {64, 128}; block in {16, 32, 64, 128}; page_size a multiple of
+ * block; num_pages >= 1 when paged (DDT_ERR_UNSUPPORTED / _INVALID_ARG
+ * otherwise); code pointers 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+#define DDT_Q8_EXP_MIN (-48)
+#define DDT_Q8_EXP_MAX 48
+
+typedef struct ddt_q8_cache {
+  void* k_cache;
+  void* v_cache;
+  int8_t* k_exp;
+  int8_t* v_exp;
+  const int32_t* page_table; /* NULL: dense cache */
+  int block;                 /* tokens per scale */
+  int page_size;
+  int max_pages;
+  int num_pages;             /* paged: pages in the pool */
+  int64_t t_max;             /* dense: tokens per sequence */
+  int hkv, d;
+} ddt_q8_cache;
+
+/* Quantise new rows into the cache behind the tokens that are there: rows
+ * i < n_new[b] of k_new / v_new go to positions ctx_len[b] + i.  Serves whole
+ * prompts (ctx_len 0), chunks of them, and single tokens.
+ *
+ * For every block of positions that gets rows, per kv head, K and V apart: e
+ * is the smallest exponent with amax <= 448 * 2^e, amax over the new rows'
+ * finite elements in the block (DDT_Q8_EXP_MIN when they are all 0); a block
+ * that begins before ctx_len[b] keeps max(e, its stored exponent), and where
+ * that grows its older codes are rounded again, code * 2^(e_old - e).  New
+ * codes are x * 2^-e, both roundings to nearest, ties to even, saturating at
+ * +-448 (reached only beyond 448 * 2^48).  An infinity or NaN becomes the NaN
+ * code.  Nothing else of the cache is touched.
+ *
+ *   k_new, v_new  bf16 [batch][n_max][hkv][d]
+ *   n_new         int32 [batch], 0..n_max, or NULL: n_max rows each
+ *   ctx_len       int32 [batch]: tokens in the cache before the call
+ *   ctx_len_out   int32 [batch] or NULL: gets ctx_len[b] + n_new[b]; may be
+ *                 ctx_len itself (the context then grows in place)
+ * A position outside the cache (dense: >= t_max; paged: beyond max_pages or a
+ * page id outside the pool), an n_new outside [0, n_max] (clamped) or a
+ * negative ctx_len (nothing of that sequence is written) raises
+ * DDT_ERR_INVALID_ARG in dev_status; ctx_len_out still advances.  Two
+ * sequences must not share the page of a position that is written, nor a
+ * dense block.  Input pointers 16-byte aligned.  No workspace. */
+typedef struct ddt_kv_append_q8_args {
+  ddt_q8_cache cache;
+  const void* k_new;
+  const void* v_new;
+  const int32_t* n_new;      /* may be NULL */
+  const int32_t* ctx_len;
+  int32_t* ctx_len_out;      /* may be NULL, may be ctx_len */
+  int batch, n_max;
+  int32_t* dev_status;       /* may be NULL */
+} ddt_kv_append_q8_args;
+
+ddt_status ddt_kv_append_q8(const ddt_kv_append_q8_args* a, cudaStream_t stream);
+
+/* ddt_kv_commit into the 8-bit cache: position ctx_len[b] + i gets the tree
+ * K/V of row 0 (i = 0) or of row acc_nodes[b][i-1] (i = 1..acc_len[b]),
+ * quantised as ddt_kv_append_q8 does.  acc_len outside [0, L] (clamped) or an
+ * accepted row outside [0, n_max) (its position is not written) raises
+ * DDT_ERR_INVALID_ARG in dev_status.  L <= DDT_TREE_L_MAX. */
+typedef struct ddt_kv_commit_q8_args {
+  ddt_q8_cache cache;
+  const void* k_tree;        /* bf16 [batch][n_max][hkv][d] */
+  const void* v_tree;
+  const int32_t* acc_len;    /* the walk's outputs */
+  const int32_t* acc_nodes;
+  const int32_t* ctx_len;
+  int32_t* ctx_len_out;      /* gets ctx_len + acc_len + 1; may be NULL, may be ctx_len */
+  int batch, n_max, L;
+  int32_t* dev_status;       /* may be NULL */
+} ddt_kv_commit_q8_args;
+
+ddt_status ddt_kv_commit_q8(const ddt_kv_commit_q8_args* a, cudaStream_t stream);
+
+/* Read positions first[b] + r, r < n_max, of every sequence back as bf16
+ * rows: k_out / v_out [batch][n_max][hkv][d], exactly the values that the
+ * cache stands for.  Rows at or past ctx_len[b] are written as 0.  first may
+ * be NULL (0 everywhere).  A position below ctx_len[b] that is outside the
+ * cache, or a negative first[b], reads as 0 and raises DDT_ERR_INVALID_ARG in
+ * dev_status.  Output pointers 16-byte aligned. */
+typedef struct ddt_kv_read_q8_args {
+  ddt_q8_cache cache;
+  const int32_t* ctx_len;
+  const int32_t* first;      /* may be NULL */
+  void* k_out;
+  void* v_out;
+  int batch, n_max;
+  int32_t* dev_status;       /* may be NULL */
+} ddt_kv_read_q8_args;
+
+ddt_status ddt_kv_read_q8(const ddt_kv_read_q8_args* a, cudaStream_t stream);
+
+/* ddt_tree_attn over the 8-bit cache: the context's keys and values are the
+ * cache's code * 2^e, the tree rows' own K/V stay bf16.  Every other argument,
+ * the outputs and the clamping of ctx_len are those of ddt_tree_attn; n_max = 1
+ * with mask bit 0 set is an ordinary decoding step.  Scores, softmax sums and
+ * outputs accumulate in fp32; queries, codes and softmax weights meet the
+ * tensor cores as f16 under power-of-two scales (codes exactly, a query
+ * element to 2^-39 of its row's largest, a weight to 2^-12).  Tree K/V rows
+ * hold magnitudes up to 2^56; larger ones may count as infinities.  A
+ * non-finite tree value reaches only the rows whose mask shows it.  A page id
+ * outside the pool below ctx_len raises DDT_ERR_INVALID_ARG in dev_status and
+ * its tokens count as zero rows.
+ * The workspace (its size may be 0) needs no initial contents and holds
+ * nothing between calls; calls that may overlap on the GPU need one each. */
+typedef struct ddt_attn_q8_args {
+  ddt_q8_cache cache;
+  const void* q;
+  const int32_t* ctx_len;
+  int max_ctx;
+  const void* k_tree;
+  const void* v_tree;
+  const uint32_t* mask;
+  const int32_t* n_nodes;
+  int batch, n_max, hq;
+  float scale;
+  void* out;
+  float* lse_out;            /* may be NULL */
+  int32_t* dev_status;       /* may be NULL */
+} ddt_attn_q8_args;
+
+size_t ddt_tree_attn_q8_workspace_size(const ddt_attn_q8_args* a);
+ddt_status ddt_tree_attn_q8(const ddt_attn_q8_args* a, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
 
 #ifdef __cplusplus
 }
