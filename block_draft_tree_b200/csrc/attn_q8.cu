@@ -10,59 +10,62 @@
 // denominator adds P_j 2^-e_j.  So the codes meet the tensor cores as f16
 // (exact: e4m3 is a subset of f16), scales cost one multiply-add per score,
 // and P as f16 (11 bits, error 2^-12) keeps every block's share whatever its
-// scale.  m lags the true maximum by up to 2^8 and P's range begins at 2^7 for
+// scale.  m lags the true maximum by up to 2^4 and P's range begins at 2^11 for
 // a new maximum: weights reach 2^15 at most, and f16's subnormal step (2^-24)
-// is 2^-31 of the maximum, below any sum over a long tail.  Queries become f16
+// is 2^-35 of the maximum, below any sum over a long tail.  Queries become f16
 // under a power of two per row, exact down to 2^-39 of the row's largest.
 //
 // What bounds it: with R <= 32 rows per kv head the K/V codes are read once
-// for 2R multiply-adds each, so HBM.  A warp takes 16 tokens a step; thread-
-// private 16-byte cp.async copies (a lane later reads what it copied itself:
-// no barrier) keep kStages - 1 steps in flight.  The copies are laid out so
-// that a lane's bytes are its own m16n8k16 fragments: for K lane (g, c) holds
-// token g and a 16-byte chunk c, with the d index permuted alike in Q's
-// fragments; for V lane (g, c) holds tokens 2c, 2c+1, 8+2c, 9+2c and chunk g,
-// whose pairs one byte permute interleaves.  One cvt turns two codes into an
-// f16 pair, so nothing is transposed and nothing is staged twice.
+// for 2R multiply-adds each, so HBM.  A warp takes 32 tokens a step; its lane
+// 0 copies the step's K and V codes by TMA into a private ring of two steps
+// (12 warps an SM: 96 KB in flight), so no lane computes an address and no
+// barrier joins the warps before the end.  The places and exponents of the
+// next 16 steps are looked up by 32 lanes at once and handed out by shuffles.
+// The products are S^T = K Q^T and O^T = V^T P^T, so that query rows are the
+// m16n8k16's narrow side: 8 rows (a decoding step of 8 heads per kv head) pad
+// nothing.  A lane reads its own fragments: for K, lane (g, c) holds tokens g,
+// g + 8 and two 16-byte chunks, with the d index permuted alike in Q's
+// fragments; for V, lane (g, c) holds tokens 2c, 2c+1, 8+2c, 9+2c and chunk g,
+// whose pairs one byte permute interleaves while it spreads them for the
+// conversion to f16; P^T turns between the products by movmatrix.
 #include <algorithm>
+#include <type_traits>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "attn_q8.cuh"
 #include "launch.h"
+#include "tcgen05.cuh"
 
 namespace ddt {
+namespace tc {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
+}
 namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 4;             // steps in the ring of a warp
-constexpr int kStep = 16;              // tokens of a step
-constexpr float kSlack = 8.f;          // the reference moves when a score passes it by 2^8
-constexpr float kHead = 7.f;           // P of a new maximum is 2^7
+constexpr int kStages = 2;             // steps in the ring of a warp
+constexpr int kHalf = 16;              // tokens that share a place and an exponent
+constexpr int kStep = 2 * kHalf;       // tokens of a step
+constexpr float kSlack = 4.f;          // the reference moves when a score passes it by 2^4
+constexpr float kHead = 11.f;          // P of a new maximum is 2^11
+constexpr int kTreeTop = 4;            // tree rows as f16: amax in [2^4, 2^5)
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(dst)),
-               "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async8(void* dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(dst)),
-               "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 // D += A (16x16, row) * B (16x8, col), f16 inputs, f32 accumulators.
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Transpose of an 8 x 8 matrix of 16-bit elements held as a fragment.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
@@ -83,18 +86,16 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2_finite(uint32_t w, float inv
   return bf16x2_to_f16x2(w, inv);
 }
 
-template <int D, int MT>
+template <int D, int NR>
 struct Smem {
-  static constexpr int kKSlots = 2 * (D / 64);           // 16-byte copies of K a lane makes per step
-  static constexpr int kVSlots = 4;                      // V: 4 tokens, D/8 bytes each
-  static constexpr int kVBytes = D / 8;                  // 16 or 8
-  static constexpr int kStageBytes = 32 * (kKSlots * 16 + kVSlots * kVBytes);
+  static constexpr int kHalfBytes = kHalf * D;           // K (or V) codes of 16 tokens
+  static constexpr int kStageBytes = 4 * kHalfBytes;     // K then V of a step
   static constexpr int kRing = kWarps * kStages * kStageBytes;
-  static constexpr int kQRow = D + 8;                    // f16 a row, padded by 16 bytes
-  static constexpr int kQ = 16 * MT * kQRow * 2;
+  static constexpr int kQ = 8 * NR * D * 2;              // Q's f16 fragments, [NR][D / 16][32 lanes] x 8 bytes
   static constexpr int kORow = D + 4;                    // f32 a row of a warp's O, padded
-  static constexpr int kMerge = kWarps * 16 * MT * (kORow * 4 + 8);
-  static constexpr int kTotal = kQ + 16 * MT * 4 + (kRing > kMerge ? kRing : kMerge);
+  static constexpr int kMerge = kWarps * 8 * NR * (kORow * 4 + 8);
+  static constexpr int kBody = kRing > kMerge ? kRing : kMerge;  // 1024-byte aligned
+  static constexpr int kTotal = 1024 + kBody + kQ + 8 * NR * 4 + kWarps * kStages * 8 + 16;
 };
 
 // Row qr of sequence b and kv head kvh: its place in q / out.
@@ -102,94 +103,115 @@ __device__ __forceinline__ int64_t row_index(const AttnQ8Params& p, int b, int k
   return ((int64_t)b * p.n_max + qr / p.g) * p.hq + kvh * p.g + qr % p.g;
 }
 
-template <int D, int MT>
-__global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) attn_q8_kernel(const AttnQ8Params p) {
-  using S = Smem<D, MT>;
-  constexpr int KH = D / 64;       // 64-wide halves of d
-  constexpr int NT = D / 8;        // n-tiles of O
+template <int D, int NR>  // NR: tiles of 8 query rows
+__global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
+    attn_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const AttnQ8Params p) {
+  using S = Smem<D, NR>;
+  constexpr int KH = D / 64;       // 16-byte chunks of a K row that a lane holds
+  constexpr int NT = D / 16;       // m-tiles of O^T
+  constexpr int RT = 8 * NR;       // query rows of a CTA
   constexpr int KS = D / 16;       // k-steps of QK
-  extern __shared__ __align__(16) unsigned char smem[];
-  __half* sQ = (__half*)smem;
-  float* sRow = (float*)(smem + S::kQ);  // score multiplier of each row
-  unsigned char* ring = smem + S::kQ + 16 * MT * 4;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* ring = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  unsigned char* sQ = ring + S::kBody;
+  float* sRow = (float*)(ring + S::kBody + S::kQ);  // score multiplier of each row
+  uint64_t* bars = (uint64_t*)(sRow + RT);     // [kWarps][kStages]
+  int* s_abort = (int*)(bars + kWarps * kStages);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   const int tile = blockIdx.x, split = blockIdx.y, grp = blockIdx.z;
   const int b = grp / p.c.hkv, kvh = grp % p.c.hkv;
   const int R = p.n_max * p.g;
-  const int q0 = tile * 16 * MT;
+  const int q0 = tile * RT;
+  uint64_t* full = bars + warp * kStages;
+  if (tid == 0) *s_abort = 0;
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
   pdl_wait();
   int n, T;
   attn_q8_lengths(p, b, tile == 0 && split == 0 && kvh == 0 && tid == 0, n, T);
+  const int nhalf = (T + kHalf - 1) / kHalf;     // 16-token pieces of the context
   const int nctx = (T + kStep - 1) / kStep;
-  const int nall = nctx + (n + kStep - 1) / kStep;
+  const int nall = nctx + (n + kHalf - 1) / kHalf;  // then the tree, 16 rows a step
   const int lo = min(split * p.steps_per_split, nall);
   const int hi = min(lo + p.steps_per_split, nall);
   const bool dead = q0 >= n * p.g;  // every row past the tree
   const bool idle = dead || lo >= hi;
   const int chi = min(hi, nctx);
-
-  // ---- the ring's producer: this lane's own fragments of context step `s`
-  const uint8_t* kbase = p.c.kc + (int64_t)kvh * D;
-  const uint8_t* vbase = p.c.vc + (int64_t)kvh * D;
   const int64_t stride = (int64_t)p.c.hkv * D;
-  unsigned char* my = ring + warp * kStages * S::kStageBytes + lane * 16;
-  unsigned char* myv = ring + warp * kStages * S::kStageBytes + 32 * S::kKSlots * 16 + lane * S::kVBytes;
-  auto place = [&](int s) -> Q8Place { return s < chi ? q8_place(p.c, b, (int64_t)s * kStep) : Q8Place{-1, -1}; };
-  auto copy = [&](int s, int stage, const Q8Place& at) {
-    if (s >= chi) return;
-    const int t0 = s * kStep;
-    const int have = at.row < 0 ? 0 : T - t0;  // tokens of the step that exist
-    const int64_t base = max(at.row, (int64_t)0) * stride;
-    unsigned char* dk = my + stage * S::kStageBytes;
-    unsigned char* dv = myv + stage * S::kStageBytes;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int t = j * 8 + g;
-      const bool ok = t < have;
-      const uint8_t* src = kbase + base + (ok ? t : 0) * stride + c * 16;
-#pragma unroll
-      for (int h = 0; h < KH; ++h) cp_async16(dk + (j * KH + h) * 512, src + h * 64, ok ? 16 : 0);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = (i >> 1) * 8 + 2 * c + (i & 1);
-      const bool ok = t < have;
-      const uint8_t* src = vbase + base + (ok ? t : 0) * stride + g * S::kVBytes;
-      if (D == 128)
-        cp_async16(dv + i * 512, src, ok ? 16 : 0);
-      else
-        cp_async8(dv + i * 256, src, ok ? 8 : 0);
-    }
-  };
-  auto exps = [&](const Q8Place& at, int& ek, int& ev) {
-    ek = ev = 0;
-    if (at.row >= 0) {
-      ek = p.c.ke[at.blk * p.c.hkv + kvh];
-      ev = p.c.ve[at.blk * p.c.hkv + kvh];
-    }
-  };
 
-  int s_mine = lo + warp;              // this warp's steps: lo + warp, + kWarps, ...
-  int ek_ring[kStages], ev_ring[kStages];
-  Q8Place next{-1, -1};
+  // ---- context steps of this warp: lo + warp + it * kWarps, it < steps
+  const int first = lo + warp;
+  const int steps = idle || first >= chi ? 0 : (chi - first + kWarps - 1) / kWarps;
+  // Lane l's look-up for iterations 16 k ..: half l & 1 of iteration 16 k + l / 2.
+  // row: the half's first cache row (-1: none); ek, ev: its stored exponents.
+  struct LookUp {
+    int row, ek, ev;
+  };
+  auto look_up = [&](int k) -> LookUp {
+    LookUp u{-1, 0, 0};
+    const int it = 16 * k + (lane >> 1);
+    const int half = 2 * (first + it * kWarps) + (lane & 1);
+    if (it < steps && half < nhalf) {
+      const Q8Place at = q8_place(p.c, b, (int64_t)half * kHalf);
+      if (at.row < 0) {
+        raise_status(p.status, DDT_ERR_INVALID_ARG);
+      } else {
+        u.row = (int)at.row;
+        const int64_t e = at.blk * p.c.hkv + kvh;
+        u.ek = __ldg(p.c.ke + e);
+        u.ev = __ldg(p.c.ve + e);
+      }
+    }
+    return u;
+  };
+  // What a K code * 2^-8 counts for, and the V exponent of such a code: NaN for
+  // a block of NaN, -inf for a half that is not there (its weights are then 0).
+  auto k_scale = [](const LookUp& u) { return q8_scale(u.ek); };
+  auto v_exp = [](const LookUp& u) {
+    return u.row < 0 ? -INFINITY
+                     : u.ev == DDT_Q8_EXP_NAN ? __int_as_float(0x7FC00000) : (float)(q8_exp(u.ev) + kCodeShift);
+  };
+  unsigned char* my = ring + warp * kStages * S::kStageBytes;
+  // Issue iteration `it` (its look-up in `row`) into its stage.
+  auto copy = [&](int it, int row) {
+    const int r0 = __shfl_sync(0xFFFFFFFFu, row, (it & 15) * 2);
+    const int r1 = __shfl_sync(0xFFFFFFFFu, row, (it & 15) * 2 + 1);
+    if (lane != 0) return;
+    unsigned char* dst = my + it % kStages * S::kStageBytes;
+    uint64_t* bar = &full[it % kStages];
+    if (p.box_rows == kStep) {
+      if (r0 >= 0) {
+        mbar_expect_tx(bar, S::kStageBytes);
+        tma_load_3d(dst, &tm_k, 0, kvh, r0, bar);
+        tma_load_3d(dst + 2 * S::kHalfBytes, &tm_v, 0, kvh, r0, bar);
+      } else {
+        mbar_arrive(bar);
+      }
+      return;
+    }
+    mbar_expect_tx(bar, ((r0 >= 0) + (r1 >= 0)) * 2 * S::kHalfBytes);
+    if (r0 >= 0) {
+      tma_load_3d(dst, &tm_k, 0, kvh, r0, bar);
+      tma_load_3d(dst + 2 * S::kHalfBytes, &tm_v, 0, kvh, r0, bar);
+    }
+    if (r1 >= 0) {
+      tma_load_3d(dst + S::kHalfBytes, &tm_k, 0, kvh, r1, bar);
+      tma_load_3d(dst + 3 * S::kHalfBytes, &tm_v, 0, kvh, r1, bar);
+    }
+  };
+  LookUp now = look_up(0), then = now;  // this batch of 16 iterations and the next
+  for (int it = 0; it < kStages && it < steps; ++it) copy(it, now.row);
+  float now_k, now_v;               // the exponents, converted once they are needed
   if (!idle) {
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      const int s = s_mine + i * kWarps;
-      const Q8Place at = place(s);
-      if (s < chi && at.row < 0 && lane == 0) raise_status(p.status, DDT_ERR_INVALID_ARG);
-      copy(s, i, at);
-      exps(at, ek_ring[i], ev_ring[i]);
-      cp_commit();
-    }
-    ek_ring[kStages - 1] = ev_ring[kStages - 1] = 0;
-    next = place(s_mine + (kStages - 1) * kWarps);
-
-    // ---- Q as f16 under a power of two per row
+  // ---- Q as f16 under a power of two per row
     constexpr int LPR = D / 8;         // lanes of a row: 8 elements each
-    for (int r = tid / LPR; r < 16 * MT; r += kThreads / LPR) {
+    for (int r = tid / LPR; r < RT; r += kThreads / LPR) {
       const int qr = q0 + r;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (qr < R) v = __ldg((const uint4*)(p.q + row_index(p, b, kvh, qr) * D) + tid % LPR);
@@ -198,190 +220,206 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) attn_q8_kernel(cons
       for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
       const int e = m ? max(f16_exponent(m, 14), -126) : 0;
       const float inv = pow2i(-e);
-      *(uint4*)(sQ + r * S::kQRow + tid % LPR * 8) =
-          make_uint4(bf16x2_to_f16x2(v.x, inv), bf16x2_to_f16x2(v.y, inv), bf16x2_to_f16x2(v.z, inv),
-                     bf16x2_to_f16x2(v.w, inv));
+      // 4 elements of word w of chunk ch: k-step (ch % KH) * 4 + w of lane (row % 8, ch / KH)
+      const int ch = tid % LPR / 2, w0 = tid % LPR % 2 * 2;
+      uint2* at = (uint2*)sQ + (r / 8 * KS + ch % KH * 4 + w0) * 32 + (r % 8) * 4 + ch / KH;
+      at[0] = make_uint2(bf16x2_to_f16x2(v.x, inv), bf16x2_to_f16x2(v.y, inv));
+      at[32] = make_uint2(bf16x2_to_f16x2(v.z, inv), bf16x2_to_f16x2(v.w, inv));
       if (tid % LPR == 0) sRow[r] = p.scale_log2 * pow2i(e);
     }
   }
   __syncthreads();
 
-  float o[MT][NT][4];
-  float m_ref[MT][2], l[MT][2], mul[MT][2];
+  float o[NR][NT][4];  // O^T: elements g * D / 8 + 2 i (+ 1: third and fourth) of rows 2c, 2c + 1
+  float m_ref[NR][2], l[NR][2], mul[NR][2];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+  for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.f;
+      for (int e = 0; e < 4; ++e) o[nr][i][e] = 0.f;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      m_ref[mt][r] = -INFINITY;
-      l[mt][r] = 0.f;
-      mul[mt][r] = idle ? 0.f : sRow[mt * 16 + r * 8 + g];
+      m_ref[nr][r] = -INFINITY;
+      l[nr][r] = 0.f;
+      mul[nr][r] = idle ? 0.f : sRow[nr * 8 + 2 * c + r];
     }
   }
-  // Q's fragments: one row tile keeps them in registers
-  uint32_t qf[MT == 1 ? KS : 1][4];
-  auto q_frag = [&](int mt, int ks, uint32_t* a) {  // k-step ks covers d = (ks/4)*64 + c*16 + (ks%4)*4 + 0..3
-    const int d0 = (ks >> 2) * 64 + c * 16 + (ks & 3) * 4;
-    const uint2 x = *(const uint2*)(sQ + (mt * 16 + g) * S::kQRow + d0);
-    const uint2 y = *(const uint2*)(sQ + (mt * 16 + 8 + g) * S::kQRow + d0);
-    a[0] = x.x;
-    a[1] = y.x;
-    a[2] = x.y;
-    a[3] = y.y;
-  };
-  if (MT == 1 && !idle) {
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) q_frag(0, ks, qf[ks]);
-  }
+  auto q_frag = [&](int nr, int ks) { return ((const uint2*)sQ)[(nr * KS + ks) * 32 + lane]; };
 
-  // The softmax of one step for row tile mt: scores sc (f32 fragments of two
-  // 8-token tiles) to P's f16 fragments.  kmul: 2^(K exponent); ev: V exponent;
-  // see[r]: the step's visible tokens for row r * 8 + g.
-  auto softmax = [&](int mt, float sc[2][4], float kmul, int ev, const uint32_t* see, bool all, uint32_t* pa) {
-    const float fev = (float)ev, down = pow2i(-ev);
-    float t[2][4];
+  // The softmax of a step for row tile nr: scores sc (f32 fragments of NH
+  // halves: tokens g, g + 8 of rows 2c, 2c + 1) to the f16 fragments of P^T.
+  // For each half: kmul, what a K product counts for, and ev, the V exponent.
+  // bits[r]: the tokens that row 2c + r sees, unless it sees all.
+  auto softmax = [&](auto nh, int nr, float (*sc)[4], const float* kmul, const float* ev, bool all,
+                     const uint32_t* bits, uint32_t (*pt)[2]) {
+    constexpr int NH = decltype(nh)::value;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int h = 0; h < NH; ++h)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        t[j][e] = fmaf(sc[j][e], mul[mt][e >> 1] * kmul, fev);
-        if (!all && !((see[e >> 1] >> (j * 8 + 2 * c + (e & 1))) & 1u)) t[j][e] = -INFINITY;
-      }
-    const float top0 = fmaxf(fmaxf(t[0][0], t[0][1]), fmaxf(t[1][0], t[1][1]));
-    const float top1 = fmaxf(fmaxf(t[0][2], t[0][3]), fmaxf(t[1][2], t[1][3]));
-    const bool move = top0 > m_ref[mt][0] + (kSlack + kHead) || top1 > m_ref[mt][1] + (kSlack + kHead);
-    if (__any_sync(0xFFFFFFFFu, move)) {
-      float top[2] = {top0, top1};
+      for (int e = 0; e < 4; ++e) sc[h][e] = fmaf(sc[h][e], mul[nr][e & 1] * kmul[h], ev[h]);
+    if (!all) {
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!((bits[e & 1] >> (h * kHalf + g + (e >> 1) * 8)) & 1u)) sc[h][e] = -INFINITY;
+    }
+    float top[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      top[r] = fmaxf(sc[0][r], sc[0][2 + r]);
+#pragma unroll
+      for (int h = 1; h < NH; ++h) top[r] = fmax3(top[r], sc[h][r], sc[h][2 + r]);
+    }
+    if (__any_sync(0xFFFFFFFFu, top[0] > m_ref[nr][0] + (kSlack + kHead) || top[1] > m_ref[nr][1] + (kSlack + kHead))) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 2));
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], x));
         float alpha = 1.f;
-        if (top[r] > m_ref[mt][r] + (kSlack + kHead)) {
+        if (top[r] > m_ref[nr][r] + (kSlack + kHead)) {
           const float to = top[r] - kHead;
-          alpha = m_ref[mt][r] == -INFINITY ? 0.f : ex2(m_ref[mt][r] - to);
-          m_ref[mt][r] = to;
+          alpha = m_ref[nr][r] == -INFINITY ? 0.f : ex2(m_ref[nr][r] - to);
+          m_ref[nr][r] = to;
         }
-        l[mt][r] *= alpha;
+        l[nr][r] *= alpha;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          o[mt][i][2 * r] *= alpha;
-          o[mt][i][2 * r + 1] *= alpha;
+          o[nr][i][r] *= alpha;
+          o[nr][i][2 + r] *= alpha;
         }
       }
     }
+    float m[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float m = m_ref[mt][r] == -INFINITY ? 0.f : m_ref[mt][r];
-      float w[2][2];
+    for (int r = 0; r < 2; ++r) m[r] = m_ref[nr][r] == -INFINITY ? 0.f : m_ref[nr][r];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+    for (int h = 0; h < NH; ++h) {
+      float w[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) w[j][e] = ex2(t[j][2 * r + e] - m);
-      l[mt][r] = fmaf((w[0][0] + w[0][1]) + (w[1][0] + w[1][1]), down, l[mt][r]);
-      pa[r] = f32x2_to_f16x2(w[0][0], w[0][1]);
-      pa[2 + r] = f32x2_to_f16x2(w[1][0], w[1][1]);
+      for (int e = 0; e < 4; ++e) w[e] = ex2(sc[h][e] - m[e & 1]);
+      // (a half that is not there has weights 0 and must not meet 2^inf)
+      const float down = ex2(fminf(-ev[h], 126.f));
+#pragma unroll
+      for (int r = 0; r < 2; ++r) l[nr][r] = fmaf(w[r] + w[2 + r], down, l[nr][r]);
+      pt[h][0] = movmatrix(f32x2_to_f16x2(w[0], w[1]));
+      pt[h][1] = movmatrix(f32x2_to_f16x2(w[2], w[3]));
     }
   };
 
   // ---- context steps
+  // byte offsets of this lane's fragments in a stage, under TMA's swizzle (16-byte
+  // chunk ^ row & 7 in 128-byte rows, ^ row / 2 & 3 in 64-byte rows)
+  int koff[KH], voff[2];
+#pragma unroll
+  for (int h = 0; h < KH; ++h) koff[h] = g * D + (D == 128 ? ((2 * c + h) ^ g) * 16 : (c ^ (g >> 1)) * 16);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    voff[i] = (2 * c + i) * D + (D == 128 ? (g ^ (2 * c + i)) * 16 : ((g >> 1) ^ c) * 16 + (g & 1) * 8);
+  now_k = k_scale(now);
+  now_v = v_exp(now);
   int it = 0;
-  for (; !idle && s_mine < chi; s_mine += kWarps, ++it) {
-    const int stage = it % kStages;
-    {  // refill the stage that the last step freed
-      const int s = s_mine + (kStages - 1) * kWarps;
-      if (s < chi && next.row < 0 && lane == 0) raise_status(p.status, DDT_ERR_INVALID_ARG);
-      copy(s, (it + kStages - 1) % kStages, next);
-      exps(next, ek_ring[kStages - 1], ev_ring[kStages - 1]);
-      cp_commit();
-      next = place(s + kWarps);
+  for (; it < steps; ++it) {
+    if ((it & 15) == 0) then = look_up((it >> 4) + 1);  // used from iteration it + 14 on
+    float kmul[2], ev[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      kmul[h] = __shfl_sync(0xFFFFFFFFu, now_k, (it & 15) * 2 + h);
+      ev[h] = __shfl_sync(0xFFFFFFFFu, now_v, (it & 15) * 2 + h);
     }
-    cp_wait<kStages - 1>();
-    const float kmul = pow2i(q8_exp((int8_t)ek_ring[0]));
-    const int ev = q8_exp((int8_t)ev_ring[0]);
-    const unsigned char* dk = my + stage * S::kStageBytes;
-    float sc[MT][2][4];
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[it % kStages], (uint32_t)(it / kStages) & 1u, s_abort,
+                                                   p.wait_cycles)))
+      break;
+    const unsigned char* dk = my + it % kStages * S::kStageBytes;
+    const unsigned char* dv = dk + 2 * S::kHalfBytes;
+    float sc[NR][2][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[mt][j][e] = 0.f;
+        for (int e = 0; e < 4; ++e) sc[nr][h][e] = 0.f;
 #pragma unroll
     for (int h = 0; h < KH; ++h) {
-      const uint4 k0 = *(const uint4*)(dk + h * 512);
-      const uint4 k1 = *(const uint4*)(dk + (KH + h) * 512);
+      uint4 k[4];  // tokens g, g + 8, g + 16, g + 24
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k[j] = *(const uint4*)(dk + koff[h] + j * 8 * D);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const uint32_t w0 = word(k0, w), w1 = word(k1, w);
-        const uint32_t b00 = e4m3x2_to_f16x2((uint16_t)w0), b01 = e4m3x2_to_f16x2((uint16_t)(w0 >> 16));
-        const uint32_t b10 = e4m3x2_to_f16x2((uint16_t)w1), b11 = e4m3x2_to_f16x2((uint16_t)(w1 >> 16));
+        uint2 q[NR];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          uint32_t a[4];
-          if (MT == 1) {
+        for (int nr = 0; nr < NR; ++nr) q[nr] = q_frag(nr, h * 4 + w);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) a[e] = qf[h * 4 + w][e];
-          } else {
-            q_frag(mt, h * 4 + w, a);
-          }
-          mma16816(sc[mt][0], a, b00, b01);
-          mma16816(sc[mt][1], a, b10, b11);
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t x = word(k[2 * j], w), y = word(k[2 * j + 1], w);
+          const uint32_t a[4] = {codes_lo(x), codes_lo(y), codes_hi(x), codes_hi(y)};
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) mma16816(sc[nr][j], a, q[nr].x, q[nr].y);
         }
       }
     }
-    const int left = T - s_mine * kStep;
-    const uint32_t bits = left >= kStep ? 0xFFFFu : (1u << left) - 1u;
+    // (codes past the context are finite whatever they are, and weigh 0)
+    const int have = T - (first + it * kWarps) * kStep;
+    const uint32_t bits = have >= kStep ? 0xFFFFFFFFu : (1u << have) - 1u;
     const uint32_t see[2] = {bits, bits};
-    uint32_t pa[MT][4];
+    uint32_t pt[NR][2][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) softmax(mt, sc[mt], kmul, ev, see, left >= kStep, pa[mt]);
-    const unsigned char* dv = myv + stage * S::kStageBytes;
-    uint32_t v[4][D / 32];
+    for (int nr = 0; nr < NR; ++nr)
+      softmax(std::integral_constant<int, 2>(), nr, sc[nr], kmul, ev, have >= kStep, see, pt[nr]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (D == 128) {
-        const uint4 x = *(const uint4*)(dv + i * 512);
-        v[i][0] = x.x;
-        v[i][1] = x.y;
-        v[i][D / 32 - 2] = x.z;
-        v[i][D / 32 - 1] = x.w;
-      } else {
-        const uint2 x = *(const uint2*)(dv + i * 256);
-        v[i][0] = x.x;
-        v[i][1] = x.y;
+    for (int half = 0; half < 2; ++half) {
+      uint32_t v[4][D / 32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const unsigned char* src = dv + voff[i & 1] + half * S::kHalfBytes + (i >> 1) * 8 * D;
+        if (D == 128) {
+          const uint4 x = *(const uint4*)src;
+          v[i][0] = x.x;
+          v[i][1] = x.y;
+          v[i][D / 32 - 2] = x.z;
+          v[i][D / 32 - 1] = x.w;
+        } else {
+          const uint2 x = *(const uint2*)src;
+          v[i][0] = x.x;
+          v[i][1] = x.y;
+        }
       }
-    }
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
+      for (int w = 0; w < D / 32; ++w) {
+        const uint32_t a0[4] = {codes_of<0>(v[0][w], v[1][w]), codes_of<1>(v[0][w], v[1][w]),
+                                codes_of<0>(v[2][w], v[3][w]), codes_of<1>(v[2][w], v[3][w])};
+        const uint32_t a1[4] = {codes_of<2>(v[0][w], v[1][w]), codes_of<3>(v[0][w], v[1][w]),
+                                codes_of<2>(v[2][w], v[3][w]), codes_of<3>(v[2][w], v[3][w])};
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t x = __byte_perm(v[0][w], v[1][w], half ? 0x7362 : 0x5140);
-        const uint32_t y = __byte_perm(v[2][w], v[3][w], half ? 0x7362 : 0x5140);
-        const uint32_t x0 = e4m3x2_to_f16x2((uint16_t)x), x1 = e4m3x2_to_f16x2((uint16_t)(x >> 16));
-        const uint32_t y0 = e4m3x2_to_f16x2((uint16_t)y), y1 = e4m3x2_to_f16x2((uint16_t)(y >> 16));
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma16816(o[mt][w * 4 + half * 2], pa[mt], x0, y0);
-          mma16816(o[mt][w * 4 + half * 2 + 1], pa[mt], x1, y1);
+        for (int nr = 0; nr < NR; ++nr) {
+          mma16816(o[nr][2 * w], a0, pt[nr][half][0], pt[nr][half][1]);
+          mma16816(o[nr][2 * w + 1], a1, pt[nr][half][0], pt[nr][half][1]);
         }
       }
     }
-#pragma unroll
-    for (int i = 0; i + 1 < kStages; ++i) {
-      ek_ring[i] = ek_ring[i + 1];
-      ev_ring[i] = ev_ring[i + 1];
+    if (it + kStages < steps) {  // every lane has read the stage: refill it
+      __syncwarp();
+      copy(it + kStages, ((it + kStages) >> 4) == (it >> 4) ? now.row : then.row);
+    }
+    if ((it & 15) == 15) {
+      now = then;
+      now_k = k_scale(now);
+      now_v = v_exp(now);
     }
   }
-  cp_wait<0>();
+  if (it < steps) {  // a wait gave up: let the copies in flight land
+    int keep_going = 0;
+    for (int i = it; i < it + kStages && i < steps; ++i)
+      mbar_wait_bounded(&full[i % kStages], (uint32_t)(i / kStages) & 1u, &keep_going, kDrainCycles);
+    if (lane == 0) raise_status(p.status, DDT_ERR_TIMEOUT);
+  }
 
   // ---- tree steps: the rows' own bf16 K/V, as f16 under a power of two per step
-  for (; !idle && s_mine < hi; s_mine += kWarps) {
-    const int t0 = (s_mine - nctx) * kStep;
-    const int cnt = min(kStep, n - t0);
+  const int tfirst = first >= nctx ? first : first + (nctx - first + kWarps - 1) / kWarps * kWarps;
+  for (int s = tfirst; !idle && s < hi; s += kWarps) {
+    const int t0 = (s - nctx) * kHalf;
+    const int cnt = min(kHalf, n - t0);
     const uint16_t* kt = p.kt + (((int64_t)b * p.n_max + t0) * p.c.hkv + kvh) * D;
     const uint16_t* vt = p.vt + (((int64_t)b * p.n_max + t0) * p.c.hkv + kvh) * D;
     uint32_t kmax = 0;
@@ -394,42 +432,30 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) attn_q8_kernel(cons
         for (int q = 0; q < 2; ++q) {
           const int t = j * 8 + g;
           uint4 x = make_uint4(0, 0, 0, 0);
-          if (t < cnt) x = __ldg((const uint4*)(kt + t * stride + h * 64 + c * 16) + q);
+          if (t < cnt) x = __ldg((const uint4*)(kt + t * stride + (c * KH + h) * 16) + q);
           kmax = max_finite_bf16(max_finite_bf16(max_finite_bf16(max_finite_bf16(kmax, x.x), x.y), x.z), x.w);
           kw[j][h][q] = x;
         }
     kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);
-    const int ek = min(max(f16_exponent(kmax, 8), DDT_Q8_EXP_MIN), DDT_Q8_EXP_MAX);
+    const int ek = min(max(f16_exponent(kmax, kTreeTop), DDT_Q8_EXP_MIN), DDT_Q8_EXP_MAX);
     const float kinv = pow2i(-ek);
-    float sc[MT][2][4];
+    float sc[NR][1][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[mt][j][e] = 0.f;
+      for (int e = 0; e < 4; ++e) sc[nr][0][e] = 0.f;
 #pragma unroll
     for (int h = 0; h < KH; ++h)
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        uint32_t bb[2][2];
+        const uint4 &x = kw[0][h][w >> 1], &y = kw[1][h][w >> 1];
+        const uint32_t a[4] = {bf16x2_to_f16x2(word(x, (w & 1) * 2), kinv), bf16x2_to_f16x2(word(y, (w & 1) * 2), kinv),
+                               bf16x2_to_f16x2(word(x, (w & 1) * 2 + 1), kinv),
+                               bf16x2_to_f16x2(word(y, (w & 1) * 2 + 1), kinv)};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint4& x = kw[j][h][w >> 1];
-          bb[j][0] = bf16x2_to_f16x2(word(x, (w & 1) * 2), kinv);
-          bb[j][1] = bf16x2_to_f16x2(word(x, (w & 1) * 2 + 1), kinv);
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          uint32_t a[4];
-          if (MT == 1) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) a[e] = qf[h * 4 + w][e];
-          } else {
-            q_frag(mt, h * 4 + w, a);
-          }
-          mma16816(sc[mt][0], a, bb[0][0], bb[0][1]);
-          mma16816(sc[mt][1], a, bb[1][0], bb[1][1]);
+        for (int nr = 0; nr < NR; ++nr) {
+          const uint2 q = q_frag(nr, h * 4 + w);
+          mma16816(sc[nr][0], a, q.x, q.y);
         }
       }
     // V: tokens 2c, 2c+1, 8+2c, 9+2c, elements g*D/8 ..
@@ -454,19 +480,20 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) attn_q8_kernel(cons
     }
     vmax = __reduce_max_sync(0xFFFFFFFFu, vmax);
     odd = __any_sync(0xFFFFFFFFu, odd);
-    const int ev = min(max(f16_exponent(vmax, 8), DDT_Q8_EXP_MIN), DDT_Q8_EXP_MAX);
+    const int ev = min(max(f16_exponent(vmax, kTreeTop), DDT_Q8_EXP_MIN), DDT_Q8_EXP_MAX);
     const float vinv = pow2i(-ev);
-    uint32_t pa[MT][4];
-    const uint32_t cbits = cnt >= kStep ? 0xFFFFu : (1u << cnt) - 1u;
+    uint32_t pt[NR][1][2];
+    const float kmul = pow2i(ek), evf = (float)ev;
+    const uint32_t cbits = cnt >= kHalf ? 0xFFFFu : (1u << cnt) - 1u;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int nr = 0; nr < NR; ++nr) {
       uint32_t see[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int j = (q0 + mt * 16 + r * 8 + g) / p.g;
+        const int j = (q0 + nr * 8 + 2 * c + r) / p.g;
         see[r] = j < n ? (__ldg(p.mask + ((int64_t)b * p.n_max + j) * p.W + (t0 >> 5)) >> (t0 & 31)) & cbits : 0u;
       }
-      softmax(mt, sc[mt], pow2i(ek), ev, see, false, pa[mt]);
+      softmax(std::integral_constant<int, 1>(), nr, sc[nr], &kmul, &evf, false, see, pt[nr]);
       if (odd) {
         // a non-finite V element reaches the rows that see its token, and no others
         for (int t = 0; t < cnt; ++t)
@@ -477,50 +504,47 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) attn_q8_kernel(cons
               for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  const uint16_t x = vt[t * stride + (2 * c + e) * (D / 8) + i];
-                  if ((x & 0x7F80u) == 0x7F80u) o[mt][i][2 * r + e] += bf16_to_f32(x);
+                  const uint16_t x = vt[t * stride + g * (D / 8) + 2 * i + e];
+                  if ((x & 0x7F80u) == 0x7F80u) o[nr][i][2 * e + r] += bf16_to_f32(x);
                 }
             }
       }
     }
 #pragma unroll
-    for (int w = 0; w < D / 16; ++w) {
+    for (int w = 0; w < NT; ++w) {
       const uint32_t x0 = bf16x2_to_f16x2_finite(v[0][w], vinv), x1 = bf16x2_to_f16x2_finite(v[1][w], vinv);
       const uint32_t y0 = bf16x2_to_f16x2_finite(v[2][w], vinv), y1 = bf16x2_to_f16x2_finite(v[3][w], vinv);
+      const uint32_t a[4] = {prmt(x0, x1, 0x5410), prmt(x0, x1, 0x7632), prmt(y0, y1, 0x5410),
+                             prmt(y0, y1, 0x7632)};
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        mma16816(o[mt][2 * w], pa[mt], __byte_perm(x0, x1, 0x5410), __byte_perm(y0, y1, 0x5410));
-        mma16816(o[mt][2 * w + 1], pa[mt], __byte_perm(x0, x1, 0x7632), __byte_perm(y0, y1, 0x7632));
-      }
+      for (int nr = 0; nr < NR; ++nr) mma16816(o[nr][w], a, pt[nr][0][0], pt[nr][0][1]);
     }
   }
 
   // ---- merge the warps, write rows or partials
-  float* sO = (float*)ring;                                   // [kWarps][16 MT][kORow]
-  float2* sML = (float2*)(ring + kWarps * 16 * MT * S::kORow * 4);  // [kWarps][16 MT]
-  __syncthreads();  // every lane is done with its ring
+  float* sO = (float*)ring;                                   // [kWarps][RT][kORow]
+  float2* sML = (float2*)(ring + kWarps * RT * S::kORow * 4);  // [kWarps][RT]
+  __syncthreads();  // every warp is done with its ring
   if (!idle) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = mt * 16 + r * 8 + g;
-        l[mt][r] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][r], 1);
-        l[mt][r] += __shfl_xor_sync(0xFFFFFFFFu, l[mt][r], 2);
+        const int row = nr * 8 + 2 * c + r;
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) l[nr][r] += __shfl_xor_sync(0xFFFFFFFFu, l[nr][r], x);
         // (a row of NaN scores alone has no reference: any number carries its NaN on)
-        if (c == 0)
-          sML[warp * 16 * MT + row] = make_float2(l[mt][r] != l[mt][r] ? 0.f : m_ref[mt][r], l[mt][r]);
-        float* dst = sO + (warp * 16 * MT + row) * S::kORow;
+        if (g == 0)
+          sML[warp * RT + row] = make_float2(l[nr][r] != l[nr][r] ? 0.f : m_ref[nr][r], l[nr][r]);
+        float* dst = sO + (warp * RT + row) * S::kORow + g * (D / 8);
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) dst[(2 * c + e) * (D / 8) + i] = o[mt][i][2 * r + e];
+        for (int i = 0; i < NT; ++i) *(float2*)(dst + 2 * i) = make_float2(o[nr][i][r], o[nr][i][2 + r]);
       }
   }
   __syncthreads();
   pdl_trigger();
   constexpr int LPR = D / 4;  // threads of a row: 4 elements each
-  for (int r = tid / LPR; r < 16 * MT; r += kThreads / LPR) {
+  for (int r = tid / LPR; r < RT; r += kThreads / LPR) {
     const int qr = q0 + r;
     if (qr >= R) break;
     const int d0 = tid % LPR * 4;
@@ -528,14 +552,14 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) attn_q8_kernel(cons
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (!idle && qr < n * p.g) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sML[w * 16 * MT + r].x);
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sML[w * RT + r].x);
       if (M != -INFINITY) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float2 ml = sML[w * 16 * MT + r];
+          const float2 ml = sML[w * RT + r];
           if (ml.x == -INFINITY) continue;
           const float a = ex2(ml.x - M);
-          const float4 x = *(const float4*)(sO + (w * 16 * MT + r) * S::kORow + d0);
+          const float4 x = *(const float4*)(sO + (w * RT + r) * S::kORow + d0);
           L = fmaf(ml.y, a, L);
           acc.x = fmaf(x.x, a, acc.x);
           acc.y = fmaf(x.y, a, acc.y);
@@ -559,80 +583,114 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 3 : 2) attn_q8_kernel(cons
   }
 }
 
-// Merge the splits' partials: D/4 threads a row, 4 elements each.
+// Merge the splits' partials: a CTA per query row, its warps take the splits in
+// turn (many splits of few rows is what long contexts give), then join.
+constexpr int kCombineWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(128) attn_q8_combine(const AttnQ8Params p) {
-  constexpr int LPR = D / 4;
+__global__ void __launch_bounds__(32 * kCombineWarps) attn_q8_combine(const AttnQ8Params p) {
+  constexpr int E = D / 32;  // elements a lane
+  __shared__ float s_o[kCombineWarps][D];
+  __shared__ float2 s_ml[kCombineWarps];
   const int R = p.n_max * p.g;
-  const int qr = blockIdx.x * (128 / LPR) + threadIdx.x / LPR;
-  const int grp = blockIdx.y, b = grp / p.c.hkv, kvh = grp % p.c.hkv;
-  const int d0 = threadIdx.x % LPR * 4;
+  const int qr = blockIdx.x, grp = blockIdx.y, b = grp / p.c.hkv, kvh = grp % p.c.hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
-  if (qr >= R) return;
   int n, T;
   attn_q8_lengths(p, b, false, n, T);
-  const int64_t at = row_index(p, b, kvh, qr);
-  float M = -INFINITY, L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (qr < n * p.g) {
-    const int64_t row = (int64_t)grp * p.nsplit * R + qr;
-    constexpr int kFly = 8;
-    for (int s0 = 0; s0 < p.nsplit; s0 += kFly) {
-      float2 ml[kFly];
-      float4 v[kFly];
+  const bool live = qr < n * p.g;
+  float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
-      for (int e = 0; e < kFly; ++e)
-        ml[e] = s0 + e < p.nsplit ? p.part_ml[row + (int64_t)(s0 + e) * R] : make_float2(-INFINITY, 0.f);
-      float Mg = M;
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  const int64_t row = (int64_t)grp * p.nsplit * R + qr;
+  constexpr int kFly = 8;
+  for (int s0 = warp; live && s0 < p.nsplit; s0 += kFly * kCombineWarps) {
+    float2 ml[kFly];
+    float v[kFly][E];
 #pragma unroll
-      for (int e = 0; e < kFly; ++e) {
-        Mg = fmaxf(Mg, ml[e].x);
-        if (ml[e].x != -INFINITY) v[e] = *(const float4*)(p.part_o + (row + (int64_t)(s0 + e) * R) * D + d0);
-      }
-      if (Mg == -INFINITY) continue;
-      const float back = M == -INFINITY ? 0.f : ex2(M - Mg);
-      L *= back;
-      acc.x *= back;
-      acc.y *= back;
-      acc.z *= back;
-      acc.w *= back;
-#pragma unroll
-      for (int e = 0; e < kFly; ++e)
-        if (ml[e].x != -INFINITY) {
-          const float a = ex2(ml[e].x - Mg);
-          L = fmaf(ml[e].y, a, L);
-          acc.x = fmaf(v[e].x, a, acc.x);
-          acc.y = fmaf(v[e].y, a, acc.y);
-          acc.z = fmaf(v[e].z, a, acc.z);
-          acc.w = fmaf(v[e].w, a, acc.w);
+    for (int f = 0; f < kFly; ++f) {
+      const int s = s0 + f * kCombineWarps;
+      ml[f] = make_float2(-INFINITY, 0.f);
+      if (s < p.nsplit) {
+        const int64_t at = row + (int64_t)s * R;
+        ml[f] = p.part_ml[at];
+        const float* src = p.part_o + at * D + lane * E;
+        if (E == 4) {
+          const float4 x = *(const float4*)src;
+          v[f][0] = x.x;
+          v[f][1] = x.y;
+          v[f][E - 2] = x.z;
+          v[f][E - 1] = x.w;
+        } else {
+          const float2 x = *(const float2*)src;
+          v[f][0] = x.x;
+          v[f][1] = x.y;
         }
-      M = Mg;
+      }
     }
+    float to = M;
+#pragma unroll
+    for (int f = 0; f < kFly; ++f) to = fmaxf(to, ml[f].x);
+    if (to == -INFINITY) continue;
+    const float back = M == -INFINITY ? 0.f : ex2(M - to);
+    L *= back;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= back;
+#pragma unroll
+    for (int f = 0; f < kFly; ++f)
+      if (ml[f].x != -INFINITY) {  // (an empty split's partial was not written)
+        const float a = ex2(ml[f].x - to);
+        L = fmaf(ml[f].y, a, L);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(v[f][e], a, acc[e]);
+      }
+    M = to;
   }
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
+  if (lane == 0) s_ml[warp] = make_float2(M, L);
+  __syncthreads();
+  const int d0 = threadIdx.x * 2;
+  if (d0 >= D) return;
+  M = -INFINITY;
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) M = fmaxf(M, s_ml[w].x);
+  float x = 0.f, y = 0.f;
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w)
+    if (s_ml[w].x != -INFINITY) {
+      const float a = ex2(s_ml[w].x - M);
+      L = fmaf(s_ml[w].y, a, L);
+      x = fmaf(s_o[w][d0], a, x);
+      y = fmaf(s_o[w][d0 + 1], a, y);
+    }
   const float inv = M == -INFINITY ? 0.f : 1.f / L;
-  *(uint2*)(p.out + at * D + d0) =
-      make_uint2(f32x2_to_bf16x2(acc.x * inv, acc.y * inv), f32x2_to_bf16x2(acc.z * inv, acc.w * inv));
+  const int64_t at = row_index(p, b, kvh, qr);
+  *(uint32_t*)(p.out + at * D + d0) = f32x2_to_bf16x2(x * inv, y * inv);
   if (p.lse_out && d0 == 0)
     p.lse_out[at] = M == -INFINITY ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
 }
 
 struct Plan {
-  int mt, tiles, nsplit, steps_per_split;
+  int nr, tiles, nsplit, steps_per_split;
 };
 
-// Row tiles of 16 (or 32 when there are more rows) and KV splits.
+// Row tiles of 8, 16, 24 or 32 rows and KV splits.
 Plan plan_of(const ddt_attn_q8_args* a) {
   Plan pl;
   const long R = (long)a->n_max * (a->hq / a->cache.hkv);
-  pl.mt = R > 16 ? 2 : 1;
-  pl.tiles = (int)((R + 16 * pl.mt - 1) / (16 * pl.mt));
+  pl.nr = (int)std::min(4L, (R + 7) / 8);
+  pl.tiles = (int)((R + 8 * pl.nr - 1) / (8 * pl.nr));
   const long base = (long)pl.tiles * a->batch * a->cache.hkv;
-  const long steps = (a->max_ctx + kStep - 1) / kStep + (a->n_max + kStep - 1) / kStep;
-  const long slots = (long)device_sm_count() * (pl.mt == 1 ? 3 : 2);
-  // as many splits as fill the device, of at least 4 steps a warp
+  const long steps = (a->max_ctx + kStep - 1) / kStep + (a->n_max + kHalf - 1) / kHalf;
+  const long slots = (long)device_sm_count() * (pl.nr <= 2 ? 3 : 2);
+  // as many splits as fill the device, of at least 2 steps a warp; long
+  // contexts in splits of at most kLong steps, so that ragged ones even out
   long ns = std::max(1L, slots / std::max(1L, base));
-  ns = std::min(ns, std::max(1L, steps / (4 * kWarps)));
+  ns = std::min(ns, std::max(1L, steps / (2 * kWarps)));
+  constexpr long kLong = 64;
+  ns = std::max(ns, steps / kLong);
   ns = std::min(ns, 65535L);
   pl.steps_per_split = (int)((steps + ns - 1) / ns);
   pl.nsplit = (int)((steps + pl.steps_per_split - 1) / pl.steps_per_split);
@@ -641,13 +699,40 @@ Plan plan_of(const ddt_attn_q8_args* a) {
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-template <int D, int MT>
-cudaError_t launch_narrow(const AttnQ8Params& p, int tiles, cudaStream_t stream) {
-  const size_t smem = Smem<D, MT>::kTotal;
-  cudaError_t e = ensure_smem_attr((const void*)attn_q8_kernel<D, MT>, smem);
+// The codes as rows of one kv head: d bytes x hkv x all tokens, boxes of box_rows tokens.
+bool encode_codes(CUtensorMap* m, const void* codes, const ddt_q8_cache* c, int batch, int box_rows) {
+  auto fn = tc::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t rows =
+      c->page_table ? (cuuint64_t)c->num_pages * c->page_size : (cuuint64_t)batch * (cuuint64_t)c->t_max;
+  const cuuint64_t dims[3] = {(cuuint64_t)c->d, (cuuint64_t)c->hkv, rows};
+  const cuuint64_t str[2] = {(cuuint64_t)c->d, (cuuint64_t)c->hkv * c->d};
+  const cuuint32_t box[3] = {(cuuint32_t)c->d, 1, (cuuint32_t)box_rows};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, str, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, c->d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NR>
+cudaError_t launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, const AttnQ8Params& p, int tiles,
+                          cudaStream_t stream) {
+  const size_t smem = Smem<D, NR>::kTotal;
+  cudaError_t e = ensure_smem_attr((const void*)attn_q8_kernel<D, NR>, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_q8_kernel<D, MT>, dim3(tiles, p.nsplit, p.batch * p.c.hkv), dim3(kThreads), smem, stream,
-                    0, p);
+  return launch_pdl(attn_q8_kernel<D, NR>, dim3(tiles, p.nsplit, p.batch * p.c.hkv), dim3(kThreads), smem, stream,
+                    0, mk, mv, p);
+}
+
+template <int D>
+cudaError_t launch_narrow(const CUtensorMap& mk, const CUtensorMap& mv, const AttnQ8Params& p, const Plan& pl,
+                          cudaStream_t stream) {
+  switch (pl.nr) {
+    case 1: return launch_rows<D, 1>(mk, mv, p, pl.tiles, stream);
+    case 2: return launch_rows<D, 2>(mk, mv, p, pl.tiles, stream);
+    case 3: return launch_rows<D, 3>(mk, mv, p, pl.tiles, stream);
+    default: return launch_rows<D, 4>(mk, mv, p, pl.tiles, stream);
+  }
 }
 
 }  // namespace
@@ -686,17 +771,20 @@ ddt_status launch_attn_q8(const ddt_attn_q8_args* a, void* ws, cudaStream_t stre
   const size_t rows = (size_t)a->batch * a->cache.hkv * pl.nsplit * a->n_max * p.g;
   p.part_o = pl.nsplit > 1 ? (float*)ws : nullptr;
   p.part_ml = pl.nsplit > 1 ? (float2*)((char*)ws + align256(rows * a->cache.d * sizeof(float))) : nullptr;
-  cudaError_t e;
-  if (a->cache.d == 128)
-    e = pl.mt == 1 ? launch_narrow<128, 1>(p, pl.tiles, stream) : launch_narrow<128, 2>(p, pl.tiles, stream);
-  else
-    e = pl.mt == 1 ? launch_narrow<64, 1>(p, pl.tiles, stream) : launch_narrow<64, 2>(p, pl.tiles, stream);
+  p.wait_cycles = wait_limit_cycles();
+  // a box never leaves its page, and steps begin at multiples of 32 tokens
+  p.box_rows = a->cache.page_table && a->cache.page_size % kStep ? kHalf : kStep;
+  CUtensorMap mk = {}, mv = {};
+  if (a->max_ctx > 0 && (!encode_codes(&mk, a->cache.k_cache, &a->cache, a->batch, p.box_rows) ||
+                         !encode_codes(&mv, a->cache.v_cache, &a->cache, a->batch, p.box_rows)))
+    return DDT_ERR_CUDA;
+  cudaError_t e = a->cache.d == 128 ? launch_narrow<128>(mk, mv, p, pl, stream)
+                                    : launch_narrow<64>(mk, mv, p, pl, stream);
   if (e != cudaSuccess) return DDT_ERR_CUDA;
   if (pl.nsplit > 1) {
-    const int per = 128 / (a->cache.d / 4);
-    const dim3 grid((a->n_max * p.g + per - 1) / per, a->batch * a->cache.hkv);
-    e = a->cache.d == 128 ? launch_pdl(attn_q8_combine<128>, grid, dim3(128), 0, stream, 0, p)
-                          : launch_pdl(attn_q8_combine<64>, grid, dim3(128), 0, stream, 0, p);
+    const dim3 grid(a->n_max * p.g, a->batch * a->cache.hkv), block(32 * kCombineWarps);
+    e = a->cache.d == 128 ? launch_pdl(attn_q8_combine<128>, grid, block, 0, stream, 0, p)
+                          : launch_pdl(attn_q8_combine<64>, grid, block, 0, stream, 0, p);
     if (e != cudaSuccess) return DDT_ERR_CUDA;
   }
   return DDT_OK;

@@ -16,7 +16,9 @@ struct AttnQ8Params {
   float* lse_out;
   int32_t* status;
   int nsplit;
-  int steps_per_split;  // token steps (16) of a KV split
+  int steps_per_split;  // steps of a KV split
+  int box_rows;         // tokens of a TMA box of codes
+  long long wait_cycles;  // bound of every wait on a copy
   float* part_o;        // [batch*hkv][nsplit][R][d], R = n_max * g
   float2* part_ml;      // [batch*hkv][nsplit][R]: (reference, sum)
 };

@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(WriteParams p) {
 
   uint4 x[NP];
   uint32_t fresh = 0, older = 0;  // bit i: pass i holds a new row / an older code
-  uint32_t amax = 0;
+  uint32_t amax = 0;  // the largest magnitude's bits
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int64_t pos = pos0 + tu / CH + i * RP;
@@ -107,13 +107,12 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(WriteParams p) {
     }
   }
   const bool had = on && pos0 < ctx;
-  const int e_old = had ? q8_exp(*exps) : DDT_Q8_EXP_MIN;
+  const int e_was = had ? *exps : DDT_Q8_EXP_MIN;
+  const int e_old = q8_exp(e_was);
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    amax = max_finite_bf16(amax, x[i].x);
-    amax = max_finite_bf16(amax, x[i].y);
-    amax = max_finite_bf16(amax, x[i].z);
-    amax = max_finite_bf16(amax, x[i].w);
+    amax = max(amax, max(max_bf16(x[i].x), max_bf16(x[i].y)));
+    amax = max(amax, max(max_bf16(x[i].z), max_bf16(x[i].w)));
   }
   // bit 31: some row is new (so that an all-zero block still gets its exponent)
   amax = __reduce_max_sync(0xFFFFFFFFu, amax | (fresh ? 0x80000000u : 0u));
@@ -126,6 +125,7 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(WriteParams p) {
   pdl_trigger();
   if (!(amax >> 31)) return;
   amax &= 0x7FFFu;
+  const bool nan = amax >= 0x7F80u || e_was == DDT_Q8_EXP_NAN;
   // amax = 1.m * 2^(E - 127): 448 = 1.75 * 2^8 and 1.75 is m = 96 of 128
   int e = amax ? (int)(amax >> 7) - 127 - ((amax & 0x7Fu) <= 96u ? 8 : 7) : DDT_Q8_EXP_MIN;
   e = min(max(e, DDT_Q8_EXP_MIN), DDT_Q8_EXP_MAX);
@@ -138,17 +138,13 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(WriteParams p) {
     uint32_t c[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      // an infinity (finite amax) becomes NaN: inf - inf
-      float lo = bf16_lo(w[q]), hi = bf16_hi(w[q]);
-      lo = (w[q] & 0x7F80u) == 0x7F80u ? lo - lo : lo * inv;
-      hi = (w[q] & 0x7F800000u) == 0x7F800000u ? hi - hi : hi * inv;
-      c[q] = f32x2_to_e4m3x2(lo, hi);
+      c[q] = nan ? 0u : f32x2_to_e4m3x2(bf16_lo(w[q]) * inv, bf16_hi(w[q]) * inv);
     }
     *(uint2*)(codes + (int64_t)(tu / CH + i * RP) * hkv * D) =
         make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
   }
-  if (e > e_old && older) {
-    const float down = pow2i(e_old - e);
+  if (e > e_old && older && !nan) {
+    const float down = pow2i(e_old - e + kCodeShift);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       if (!((older >> i) & 1u)) continue;
@@ -158,14 +154,13 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(WriteParams p) {
       uint32_t c[2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)w[q]));
-        const float2 z = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[q] >> 16)));
+        const float2 a = f16x2_to_f32x2(codes_lo(w[q])), z = f16x2_to_f32x2(codes_hi(w[q]));
         c[q] = f32x2_to_e4m3x2(a.x * down, a.y * down) | (f32x2_to_e4m3x2(z.x * down, z.y * down) << 16);
       }
       *at_c = make_uint2(c[0], c[1]);
     }
   }
-  if (tu == 0) *exps = (int8_t)e;
+  if (tu == 0) *exps = (int8_t)(nan ? DDT_Q8_EXP_NAN : e);
 }
 
 __global__ void __launch_bounds__(kThreads) advance_kernel(WriteParams p) {
@@ -187,14 +182,13 @@ struct ReadParams {
 
 constexpr int kReadRows = 16;  // output rows of a CTA
 
-// One 16-byte vector of codes (16 elements) -> two of bf16.
+// One 16-byte vector of codes (16 elements) -> two of bf16; s: 2^(e + 8).
 __device__ __forceinline__ void decode16(uint4 c, float s, uint4& lo, uint4& hi) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   uint32_t o[8];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)w[q]));
-    const float2 z = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[q] >> 16)));
+    const float2 a = f16x2_to_f32x2(codes_lo(w[q])), z = f16x2_to_f32x2(codes_hi(w[q]));
     o[2 * q] = f32x2_to_bf16x2(a.x * s, a.y * s);
     o[2 * q + 1] = f32x2_to_bf16x2(z.x * s, z.y * s);
   }
@@ -252,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) read_q8_kernel(ReadParams p) {
       const int i = i0 + q * kThreads;
       if (i >= items) break;
       uint4 lo, hi;
-      decode16(v[q], pow2i(q8_exp((int8_t)e[q])), lo, hi);
+      decode16(v[q], q8_scale(e[q]), lo, hi);
       uint4* dst = out + (((int64_t)b * p.n_max + r0) * vecs + i) * 2;
       dst[0] = lo;
       dst[1] = hi;
@@ -301,6 +295,9 @@ Q8View q8_view(const ddt_q8_cache* c) {
   v.page_size = c->page_size;
   v.max_pages = c->max_pages;
   v.num_pages = c->num_pages;
+  v.page_log2 = -1;
+  for (int i = 0; i < 31; ++i)
+    if (c->page_size == 1 << i) v.page_log2 = i;
   v.t_max = c->t_max;
   v.hkv = c->hkv;
   v.d = c->d;

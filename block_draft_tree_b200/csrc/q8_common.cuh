@@ -14,6 +14,7 @@ struct Q8View {
   int8_t *ke, *ve;
   const int32_t* page_table;  // null: dense
   int page_size, max_pages, num_pages;
+  int page_log2;              // -1: page_size is no power of two
   int64_t t_max;
   int hkv, d;
   int block_log2;
@@ -36,7 +37,8 @@ __device__ __forceinline__ Q8Place q8_place(const Q8View& c, int b, int64_t t) {
     return p;
   }
   if (t >= (int64_t)c.max_pages * c.page_size) return p;
-  const int pi = (int)((uint32_t)t / (uint32_t)c.page_size);
+  const int pi = c.page_log2 >= 0 ? (int)((uint32_t)t >> c.page_log2)
+                                  : (int)((uint32_t)t / (uint32_t)c.page_size);
   const int slot = (int)((uint32_t)t - (uint32_t)pi * (uint32_t)c.page_size);
   const int pg = c.page_table[(int64_t)b * c.max_pages + pi];
   if ((uint32_t)pg < (uint32_t)c.num_pages) {
@@ -46,17 +48,34 @@ __device__ __forceinline__ Q8Place q8_place(const Q8View& c, int b, int64_t t) {
   return p;
 }
 
-__device__ __forceinline__ int q8_exp(int8_t e) {
-  return min(max((int)e, DDT_Q8_EXP_MIN), DDT_Q8_EXP_MAX);
-}
+__device__ __forceinline__ int q8_exp(int e) { return min(max(e, DDT_Q8_EXP_MIN), DDT_Q8_EXP_MAX); }
 // 2^e for |e| <= 126.
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
-// Two e4m3 codes (low byte first) -> two f16 (exact; NaN stays NaN).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t c) {
+// Pairs of e4m3 codes -> f16 pairs of code * 2^-8 (exact): a code's exponent
+// and fraction bits moved under f16's sign bit are that number, subnormals
+// included.  Three integer instructions for two codes: a byte permute that
+// puts each code, sign-extended, into a half; a shift; a mask that drops the
+// sign's copy.  (cvt.f16x2.e4m3x2 gives 16 codes a clock and SM, measured
+// here; this gives 40.)
+constexpr int kCodeShift = 8;
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
   return r;
+}
+__device__ __forceinline__ uint32_t codes_to_f16(uint32_t spread) { return (spread << 7) & 0xBF80BF80u; }
+// Bytes 0, 1 (lo) or 2, 3 (hi) of w.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return codes_to_f16(prmt(w, 0, 0x9180)); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return codes_to_f16(prmt(w, 0, 0xB3A2)); }
+// Byte I of a and of b.
+template <int I>
+__device__ __forceinline__ uint32_t codes_of(uint32_t a, uint32_t b) {
+  return codes_to_f16(prmt(a, b, 0xC480 + 0x1111 * I));
+}
+// What such an f16 counts for in a block with the stored exponent e.
+__device__ __forceinline__ float q8_scale(int e) {
+  return e == DDT_Q8_EXP_NAN ? __int_as_float(0x7FC00000) : pow2i(q8_exp(e) + kCodeShift);
 }
 // Two floats -> two e4m3 codes (lo in the low byte), nearest-even, saturating.
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
@@ -78,6 +97,8 @@ __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// The larger magnitude's bits of two packed bf16.
+__device__ __forceinline__ uint32_t max_bf16(uint32_t w) { return max(w & 0x7FFFu, (w >> 16) & 0x7FFFu); }
 // The larger magnitude bits of the finite ones among two packed bf16 and m.
 __device__ __forceinline__ uint32_t max_finite_bf16(uint32_t m, uint32_t w) {
   const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;

@@ -496,14 +496,17 @@ ddt_status ddt_tree_walk_sample(const void* logits, ddt_dtype dtype, int batch, 
 /* ------------------------------------------------------------------------
  * The 8-bit key/value cache.
  *
- * Codes: e4m3 (1 sign, 4 exponent, 3 fraction bits; no infinity, S.1111.111
- * is NaN), one byte per element in the layout of the bf16 cache.  Scales: one
- * int8 exponent e for every block of `block` tokens of every kv head, K and V
+ * Codes: e4m3 (1 sign, 4 exponent, 3 fraction bits, largest value 448), one
+ * byte per element in the layout of the bf16 cache; e4m3's NaN code
+ * (S.1111.111) is never written and counts as +-480.  Scales: one int8
+ * exponent e for every block of `block` tokens of every kv head, K and V
  * apart; an element's value is code * 2^e.  Exponents lie in
- * [DDT_Q8_EXP_MIN, DDT_Q8_EXP_MAX]; a stored exponent outside is read as the
- * nearer end.  A power of two scales a code without rounding it, so a value
- * is exactly a bf16 number and a block whose scale grows keeps its older
- * codes exactly unless they become e4m3 subnormals.
+ * [DDT_Q8_EXP_MIN, DDT_Q8_EXP_MAX]; DDT_Q8_EXP_NAN marks a block that was
+ * given an infinity or NaN, all of whose elements count as NaN; any other
+ * stored exponent is read as the nearer end.  A power of two scales a code
+ * without rounding it, so a value is exactly a bf16 number and a block whose
+ * scale grows keeps its older codes exactly unless they become e4m3
+ * subnormals.
  *
  *   dense  (page_table == NULL): codes [batch][t_max][hkv][d], exponents
  *          [batch][ceil(t_max / block)][hkv];
@@ -516,6 +519,7 @@ ddt_status ddt_tree_walk_sample(const void* logits, ddt_dtype dtype, int batch, 
  * ------------------------------------------------------------------------ */
 #define DDT_Q8_EXP_MIN (-48)
 #define DDT_Q8_EXP_MAX 48
+#define DDT_Q8_EXP_NAN (-128)
 
 typedef struct ddt_q8_cache {
   void* k_cache;
@@ -541,8 +545,10 @@ typedef struct ddt_q8_cache {
  * that begins before ctx_len[b] keeps max(e, its stored exponent), and where
  * that grows its older codes are rounded again, code * 2^(e_old - e).  New
  * codes are x * 2^-e, both roundings to nearest, ties to even, saturating at
- * +-448 (reached only beyond 448 * 2^48).  An infinity or NaN becomes the NaN
- * code.  Nothing else of the cache is touched.
+ * +-448 (reached only beyond 448 * 2^48).  A block whose new rows hold an
+ * infinity or NaN, or that begins before ctx_len[b] with DDT_Q8_EXP_NAN, gets
+ * DDT_Q8_EXP_NAN, and zeros for its new codes.  Nothing else of the cache is
+ * touched.
  *
  *   k_new, v_new  bf16 [batch][n_max][hkv][d]
  *   n_new         int32 [batch], 0..n_max, or NULL: n_max rows each
@@ -615,7 +621,7 @@ ddt_status ddt_kv_read_q8(const ddt_kv_read_q8_args* a, cudaStream_t stream);
  * hold magnitudes up to 2^56; larger ones may count as infinities.  A
  * non-finite tree value reaches only the rows whose mask shows it.  A page id
  * outside the pool below ctx_len raises DDT_ERR_INVALID_ARG in dev_status and
- * its tokens count as zero rows.
+ * its tokens are left out.
  * The workspace (its size may be 0) needs no initial contents and holds
  * nothing between calls; calls that may overlap on the GPU need one each. */
 typedef struct ddt_attn_q8_args {

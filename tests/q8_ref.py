@@ -6,35 +6,40 @@ import math
 
 import torch
 
-EXP_MIN, EXP_MAX = -48, 48
+EXP_MIN, EXP_MAX, EXP_NAN = -48, 48, -128
 
 
 def code_values() -> torch.Tensor:
-    """f64 value of each of the 256 e4m3 codes."""
+    """f64 value of each of the 256 codes: e4m3, its NaN code counting as 480."""
     v = []
     for c in range(256):
         ex, fr = (c >> 3) & 15, c & 7
         m = fr * 2.0 ** -9 if ex == 0 else (8 + fr) * 2.0 ** (ex - 10)
-        v.append(math.nan if (c & 127) == 127 else (-m if c & 128 else m))
+        v.append(-m if c & 128 else m)
     return torch.tensor(v, dtype=torch.float64)
 
 
 def encode(y: torch.Tensor) -> torch.Tensor:
     """f64 -> e4m3 codes (uint8), nearest, ties to the even code; saturating;
-    infinities are the caller's to replace, NaN becomes a NaN code."""
+    finite values only."""
     mags = code_values()[:127].to(y.device)                 # 0 .. 448, ascending
-    a = y.abs().clamp(max=448.0).nan_to_num(0.0)
+    a = y.abs().clamp(max=448.0)
     hi = torch.searchsorted(mags, a.contiguous()).clamp(max=126)
     lo = (hi - 1).clamp(min=0)
     below, above = a - mags[lo], mags[hi] - a
     take_lo = (below < above) | ((below == above) & (lo % 2 == 0))
     c = torch.where(take_lo, lo, hi).to(torch.uint8)
-    c = torch.where(torch.signbit(y), c | 128, c)
-    return torch.where(y.isnan(), torch.full_like(c, 127), c)
+    return torch.where(torch.signbit(y), c | 128, c)
 
 
 def decode(codes: torch.Tensor) -> torch.Tensor:
     return code_values().to(codes.device)[codes.view(torch.uint8).long()]
+
+
+def scales(exps: torch.Tensor) -> torch.Tensor:
+    """f64 scale of stored exponents (NaN for a block marked so)."""
+    s = torch.exp2(exps.double().clamp(EXP_MIN, EXP_MAX))
+    return torch.where(exps == EXP_NAN, math.nan, s)
 
 
 def needed_exp(amax: float) -> int:
@@ -61,7 +66,7 @@ class Cache:
             shape = (b, tokens)
         nb = -(-shape[1] // block)
         codes = torch.randint(0, 256, (2, *shape, hkv, d), generator=g, dtype=torch.uint8)
-        codes = torch.where((codes & 127) == 127, codes & 0x80, codes)  # no NaN
+        codes = torch.where((codes & 127) == 127, codes & 0x80, codes)  # as the library writes them
         e = torch.randint(exps[0], exps[1] + 1, (2, shape[0], nb, hkv), generator=g).to(torch.int8)
         self.codes = [c.to(device) for c in codes]
         self.exps = [x.contiguous().to(device) for x in e]
@@ -93,14 +98,14 @@ class Cache:
 
     def values(self, which, i, n):
         """f64 [n, hkv, d] of positions 0..n-1 of sequence i."""
-        codes, exps = self.codes[which], self.exps[which].double().clamp(EXP_MIN, EXP_MAX)
+        codes, exps = self.codes[which], scales(self.exps[which])
         if self.page:
             pages = self.page_table[i, :-(-n // self.page)].long() if n else self.page_table[i, :0].long()
             codes, exps = codes[pages].flatten(0, 1), exps[pages].flatten(0, 1)
         else:
             codes, exps = codes[i], exps[i]
         e = exps.repeat_interleave(self.block, 0)[:n]
-        return decode(codes[:n]) * torch.exp2(e)[:, :, None]
+        return decode(codes[:n]) * e[:, :, None]
 
     def append(self, i, ctx, rows_k, rows_v):
         """The definition of a write, a block and a head at a time; rows [n, hkv, d]."""
@@ -119,24 +124,22 @@ class Cache:
                         new = new[:max(0, self.codes[0].shape[1] - pos)]
                     for h in range(self.hkv if new.shape[0] else 0):
                         x = new[:, h]
-                        fin = torch.where(torch.isfinite(x), x, torch.zeros_like(x))
-                        e = needed_exp(float(fin.abs().max()))
+                        was = int(self.exps[which][a, s // block, h])
+                        new_codes = self.codes[which][a, s + pos - b0:s + pos - b0 + x.shape[0], h]
+                        if not torch.isfinite(x).all() or (b0 < ctx and was == EXP_NAN):
+                            self.exps[which][a, s // block, h] = EXP_NAN
+                            new_codes.zero_()
+                            continue
+                        e = needed_exp(float(x.abs().max()))
                         if b0 < ctx:
-                            old_e = max(EXP_MIN, min(EXP_MAX, int(self.exps[which][a, s // block, h])))
+                            old_e = max(EXP_MIN, min(EXP_MAX, was))
                             e = max(e, old_e)
                             if e > old_e:
                                 old = self.codes[which][a, s:s + pos - b0, h]
                                 self.codes[which][a, s:s + pos - b0, h] = encode(decode(old) * 2.0 ** (old_e - e))
-                        y = torch.where(torch.isfinite(x), x * 2.0 ** -e, torch.full_like(x, math.nan))
-                        self.codes[which][a, s + pos - b0:s + pos - b0 + x.shape[0], h] = encode(y)
+                        new_codes.copy_(encode(x * 2.0 ** -e))
                         self.exps[which][a, s // block, h] = e
                 pos = end
-
-
-def same_codes(got: torch.Tensor, want: torch.Tensor) -> torch.Tensor:
-    """Equal codes, any NaN code for a NaN code."""
-    got, want = got.view(torch.uint8), want.view(torch.uint8)
-    return (got == want) | (((got & 127) == 127) & ((want & 127) == 127))
 
 
 def attention(q, kv_ctx, kv_tree, see, scale):

@@ -149,7 +149,7 @@ def test_rows_that_see_nothing():
 
 @pytest.mark.parametrize("n", [1, 9, 70, 140])
 def test_garbage_outside_the_context(n):
-    """NaN codes and wild exponents past ctx_len, pages that do not exist, NaN
+    """Stray codes and wild exponents past ctx_len, pages that do not exist, NaN
     rows past n_nodes: none of it shows."""
     for page in (0, 64):
         c = Case(n, 8, 2, 128, page=page, ctx=(70, 0), n_nodes=(max(1, n - 1), n), seed=n, tokens=256)
@@ -162,7 +162,7 @@ def test_garbage_outside_the_context(n):
                     at = c.c.place(i, t)
                     c.c.codes[w][at[0], at[1]] = 0x7F if t % 2 else 0xFF
                     if t % 16 == 0 and t >= T:
-                        c.c.exps[w][at[0], at[1] // 16] = 127 if w else -128
+                        c.c.exps[w][at[0], at[1] // 16] = -128 if (t // 16 + w) % 2 else 127
         if page:
             c.c.page_table[:, 2:] = -1
             c.c.page_table[1] = 1 << 30
@@ -178,19 +178,20 @@ def test_non_finite_tree_rows_reach_only_those_who_see_them(n):
     c.go()
 
 
-def test_non_finite_codes_and_queries():
-    """A NaN code in the context: every row of that head (K), or that column
-    (V); a NaN query: its own row alone."""
+def test_nan_blocks_and_queries():
+    """A block marked as NaN in the context makes every row of its head NaN (K
+    or V), a NaN query its own row alone; blocks marked past the context do not
+    show (test_garbage_outside_the_context)."""
     for n in (1, 70, 140):
-        c = Case(n, 4, 2, 128, ctx=(50, 60), seed=n)
-        c.c.codes[0][0, 17, 1, 3] = 0x7F
-        c.c.codes[1][1, 18, 0, 4] = 0xFF
+        c = Case(n, 4, 2, 128, ctx=(50, 60, 40), seed=n)
+        c.c.exps[0][0, 1, 1] = -128
+        c.c.exps[1][2, 2, 0] = -128
         c.q[1, 0, 3, 2] = float("nan")
         out, lse = c.run()
         assert out[0, :, 2:].isnan().all() and lse[0, :, 2:].isnan().all() and not out[0, :, :2].isnan().any()
-        assert out[1, :, :2, 4].isnan().all() and not out[1, :, :2, :4].isnan().any()
-        assert out[1, 0, 3].isnan().all() and not out[1, 0, 2].isnan().any()
-        assert not out[1, 1:, 2:].isnan().any()
+        assert out[2, :, :2].isnan().all() and not out[2, :, 2:].isnan().any()
+        assert out[1, 0, 3].isnan().all() and not out[1, 0, :3].isnan().any()
+        assert not out[1, 1:].isnan().any()
 
 
 @pytest.mark.parametrize("n", [1, 40, 130])

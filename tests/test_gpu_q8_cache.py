@@ -6,7 +6,6 @@ import torch
 
 from block_draft_tree_b200 import api
 
-import q8_ref
 from q8_ref import Cache
 
 pytestmark = pytest.mark.gpu
@@ -29,7 +28,7 @@ def _i32(x):
 
 def _check(got: Cache, want: Cache):
     for w in range(2):
-        assert q8_ref.same_codes(got.codes[w], want.codes[w]).all(), "codes of %s" % "KV"[w]
+        assert torch.equal(got.codes[w], want.codes[w]), "codes of %s" % "KV"[w]
         assert torch.equal(got.exps[w], want.exps[w]), "exponents of %s" % "KV"[w]
 
 
@@ -91,7 +90,19 @@ def test_append_values_at_the_edges():
         want.append(i, 0, k[i], v[i])
     api.kv_append_q8(k, v, _i32([0] * 8), *c.args(), **c.kw())
     _check(c, want)
-    assert c.exps[0][:, 0, 0].tolist() == [-48, -48, 48, 0, 1, -7, -7, -48]
+    assert c.exps[0][:, 0, 0].tolist() == [-48, -48, 48, 0, 1, -128, -128, -128]
+    # a marked block stays marked while it fills, and reads as NaN; the next block is clean
+    ones = torch.ones((8, 3, 1, d), dtype=torch.bfloat16, device=DEV)
+    for i in range(8):
+        want.append(i, 15, ones[i], ones[i])
+    api.kv_append_q8(ones, ones, _i32([15] * 8), *c.args(), **c.kw())
+    _check(c, want)
+    assert c.exps[0][:, 0, 0].tolist()[5:] == [-128] * 3 and c.exps[0][:, 1, 0].tolist() == [-8] * 8
+    kr, _ = api.kv_read_q8(*c.args(), _i32([18] * 8), 18, **c.kw())
+    assert kr[5:, :16].isnan().all() and (kr[:, 16:] == 1).all()
+    # filled again from its beginning, it is clean
+    api.kv_append_q8(ones, ones, _i32([0] * 8), *c.args(), **c.kw())
+    assert c.exps[0][:, 0, 0].tolist() == [-8] * 8
 
 
 def test_append_out_of_range_is_reported_and_nothing_else_written():
