@@ -39,6 +39,7 @@
 #include "tcgen05.cuh"
 
 namespace ddt {
+cudaError_t launch_attn_q8_wide(const AttnQ8Params& p, int pairs, cudaStream_t stream);
 namespace tc {
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 }
@@ -51,6 +52,7 @@ constexpr int kHalf = 16;              // tokens that share a place and an expon
 constexpr int kStep = 2 * kHalf;       // tokens of a step
 constexpr float kSlack = 4.f;          // the reference moves when a score passes it by 2^4
 constexpr float kHead = 11.f;          // P of a new maximum is 2^11
+constexpr long kWideRows = 32;         // rows per kv head beyond which d = 128 takes the wide kernel
 constexpr int kTreeTop = 4;            // tree rows as f16: amax in [2^4, 2^5)
 
 // D += A (16x16, row) * B (16x8, col), f16 inputs, f32 accumulators.
@@ -673,13 +675,38 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_q8_combine(const Attn
 }
 
 struct Plan {
-  int nr, tiles, nsplit, steps_per_split;
+  int nr;  // tiles of 8 query rows a CTA; 0: the wide kernel
+  int tiles, nsplit, steps_per_split;
 };
+
+// The wide kernel's pairs of row tiles and KV splits (steps: tiles of 128
+// tokens): the fewest waves x tiles, a split's partials and their merge
+// counted as kMergeTiles tiles.
+Plan plan_wide(const ddt_attn_q8_args* a, long R) {
+  constexpr long kMergeTiles = 3;
+  Plan pl;
+  pl.nr = 0;
+  pl.tiles = (int)((R + 255) / 256);
+  const long base = (long)pl.tiles * a->batch * a->cache.hkv, sms = device_sm_count();
+  const long tiles = (a->max_ctx + 127) / 128 + (a->n_max + 127) / 128;
+  long best = -1;
+  for (long s = 1; s <= 32 && s <= tiles; ++s) {
+    const long ts = (tiles + s - 1) / s, sp = (tiles + ts - 1) / ts;
+    const long cost = (base * sp + sms - 1) / sms * ts + (sp > 1 ? kMergeTiles : 0);
+    if (best < 0 || cost < best) {
+      best = cost;
+      pl.steps_per_split = (int)ts;
+      pl.nsplit = (int)sp;
+    }
+  }
+  return pl;
+}
 
 // Row tiles of 8, 16, 24 or 32 rows and KV splits.
 Plan plan_of(const ddt_attn_q8_args* a) {
   Plan pl;
   const long R = (long)a->n_max * (a->hq / a->cache.hkv);
+  if (a->cache.d == 128 && R > kWideRows) return plan_wide(a, R);
   pl.nr = (int)std::min(4L, (R + 7) / 8);
   pl.tiles = (int)((R + 8 * pl.nr - 1) / (8 * pl.nr));
   const long base = (long)pl.tiles * a->batch * a->cache.hkv;
@@ -772,14 +799,19 @@ ddt_status launch_attn_q8(const ddt_attn_q8_args* a, void* ws, cudaStream_t stre
   p.part_o = pl.nsplit > 1 ? (float*)ws : nullptr;
   p.part_ml = pl.nsplit > 1 ? (float2*)((char*)ws + align256(rows * a->cache.d * sizeof(float))) : nullptr;
   p.wait_cycles = wait_limit_cycles();
-  // a box never leaves its page, and steps begin at multiples of 32 tokens
-  p.box_rows = a->cache.page_table && a->cache.page_size % kStep ? kHalf : kStep;
-  CUtensorMap mk = {}, mv = {};
-  if (a->max_ctx > 0 && (!encode_codes(&mk, a->cache.k_cache, &a->cache, a->batch, p.box_rows) ||
-                         !encode_codes(&mv, a->cache.v_cache, &a->cache, a->batch, p.box_rows)))
-    return DDT_ERR_CUDA;
-  cudaError_t e = a->cache.d == 128 ? launch_narrow<128>(mk, mv, p, pl, stream)
-                                    : launch_narrow<64>(mk, mv, p, pl, stream);
+  cudaError_t e;
+  if (pl.nr == 0) {
+    p.box_rows = 0;
+    e = launch_attn_q8_wide(p, pl.tiles, stream);
+  } else {
+    // a box never leaves its page, and steps begin at multiples of 32 tokens
+    p.box_rows = a->cache.page_table && a->cache.page_size % kStep ? kHalf : kStep;
+    CUtensorMap mk = {}, mv = {};
+    if (a->max_ctx > 0 && (!encode_codes(&mk, a->cache.k_cache, &a->cache, a->batch, p.box_rows) ||
+                           !encode_codes(&mv, a->cache.v_cache, &a->cache, a->batch, p.box_rows)))
+      return DDT_ERR_CUDA;
+    e = a->cache.d == 128 ? launch_narrow<128>(mk, mv, p, pl, stream) : launch_narrow<64>(mk, mv, p, pl, stream);
+  }
   if (e != cudaSuccess) return DDT_ERR_CUDA;
   if (pl.nsplit > 1) {
     const dim3 grid(a->n_max * p.g, a->batch * a->cache.hkv), block(32 * kCombineWarps);

@@ -1,0 +1,578 @@
+// attn_q8_wide.cu -- tree attention over the 8-bit key/value cache on the
+// tcgen05 tensor cores: d = 128 and more than 32 query rows per kv head.
+//
+// Mathematics: as in attn_q8.cu (codes as f16 of code * 2^-8, K exponents on
+// the scores, V exponents in the softmax's reference, queries f16 under a power
+// of two per row); tree rows become f16 under a power of two per 16 rows.  P is
+// f16 too, so kind::f16 takes both products with f16 operands.
+//
+// What bounds it: R rows of a kv head want 4 R d flops per context token, so
+// the tensor pipe, and beside it the 2^x of every score (MUFU) and the shared
+// memory that feeds the MMAs.  One CTA per SM takes two tiles of 128 rows
+// (A, B) of a kv head and KV tiles of 128 tokens, each converted once for both:
+//   * warpgroup 3 converts: codes come from global memory into registers (the
+//     next tile's loads are issued as the last one's registers are used up),
+//     become f16 by integer instructions, and go to a ring of four 32 KB
+//     slots (K, V alternating) in the 128-byte swizzle that the MMAs read;
+//     tree rows likewise.  The codes never pass through a staging buffer, and
+//     any page size works, since no box has to fit a page;
+//   * warp 1 issues PV_A(i), QK_A(i+1), PV_B(i), QK_B(i+1): one tile's softmax
+//     overlaps the other tile's MMAs;
+//   * warpgroups 1 and 2 are the softmax of A and B, a row per thread: the 128
+//     scores in registers, the context bound and the ancestor bitset as masks,
+//     P over the scores' columns, O rescaled only when the reference moves.
+// Registers go to where they are needed by setmaxnreg: 48 + 2 x 176 + 112.
+// KV splits write (O, m, l) partials that attn_q8_combine merges.  Every wait
+// is bounded; one that gives up raises DDT_ERR_TIMEOUT.
+#include "attn_q8.cuh"
+#include "launch.h"
+#include "tcgen05.cuh"
+
+namespace ddt {
+namespace {
+
+constexpr int BM = 128, BN = 128, D = 128;
+constexpr int kThreads = 512;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;   // tile t: S at 128 t, O at 256 + 128 t
+constexpr int kHalfTile = BN * 128;          // a 64-wide slice: 128 rows x 128 bytes
+constexpr int kTile = 2 * kHalfTile;         // 32 KB
+constexpr int kSlots = 4;
+constexpr float kSlack = 6.f;                // the reference moves when a score passes it by 2^6
+constexpr float kHead = 9.f;                 // P of a new maximum is 2^9: at most 2^15 in f16
+constexpr int kTreeTop = 4;                  // tree rows as f16: amax in [2^4, 2^5)
+constexpr int kGroup = 16;                   // tokens that share a place and an exponent
+constexpr int kGroups = BN / kGroup;
+
+struct __align__(16) Shared {
+  uint64_t q_full;
+  uint64_t kv_full[kSlots], kv_empty[kSlots];
+  uint64_t sc_full[4];        // the scales of tile i (ring of 4 tiles)
+  uint64_t s_full[2], p_full[2];
+  uint64_t o_full, drain;
+  long long wait_cycles;
+  uint32_t tmem_base;
+  int abort;
+  float2 scales[4][kGroups];  // (what a K product counts for, V exponent)
+  uint32_t amax[4][kGroups];  // converter warps' largest magnitudes of a tree tile
+  uint32_t odd[32];           // tree rows with a non-finite V element
+};
+
+__device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, Shared* sh) {
+  return mbar_wait_bounded(b, parity, &sh->abort, sh->wait_cycles);
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// kind::f16, f16 x f16 -> f32, M = 128, N = 128, A K-major; B K-major or MN-major.
+constexpr uint32_t idesc_f16(bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+}
+// A shared-memory descriptor from its varying low word (128-byte swizzle, 1024
+// bytes between groups of 8 rows), so that the issuer's registers hold one word each.
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+  return ((uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32) | lo;
+}
+__device__ __forceinline__ uint32_t desc_lo(const void* at, uint32_t lbo_bytes) {
+  return ((smem_u32(at) >> 4) & 0x3FFFu) | ((lbo_bytes >> 4) << 16);
+}
+// Byte offset of 16-byte chunk `ch` (0..15) of row r in a tile of two 64-wide slices.
+__device__ __forceinline__ uint32_t tile_at(int r, int ch) {
+  return (uint32_t)((ch >> 3) * kHalfTile + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+}
+// AND of v over the converter's 128 threads.
+__device__ __forceinline__ bool all_of_converter(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float inv) {
+  return f32x2_to_f16x2(bf16_lo(w) * inv, bf16_hi(w) * inv);
+}
+// amax (bf16 magnitude bits, finite) * 2^-e in [2^top, 2^(top+1)).
+__device__ __forceinline__ int f16_exponent(uint32_t amax_bits, int top) {
+  return amax_bits < 0x80u ? -126 - top : (int)(amax_bits >> 7) - 127 - top;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8Params p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  unsigned char* sQ = smem;                // [2 tiles]
+  unsigned char* sKV = smem + 2 * kTile;   // [kSlots]
+  Shared* sh = (Shared*)(sKV + kSlots * kTile);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
+  const int pair = blockIdx.x, split = blockIdx.y, grp = blockIdx.z;
+  const int b = grp / p.c.hkv, kvh = grp % p.c.hkv;
+  if (tid == 0) {
+    mbar_init(&sh->q_full, 8);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&sh->kv_full[s], 4);
+      mbar_init(&sh->kv_empty[s], 1);
+      mbar_init(&sh->sc_full[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh->s_full[t], 1);
+      mbar_init(&sh->p_full[t], 128);
+    }
+    mbar_init(&sh->o_full, 1);
+    mbar_init(&sh->drain, 1);
+    sh->wait_cycles = p.wait_cycles;
+    sh->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid < 32) sh->odd[tid] = 0;
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&sh->tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();
+  const int g = p.g, R = p.n_max * g, q0 = pair * 2 * BM;
+  int n, T;
+  attn_q8_lengths(p, b, pair == 0 && split == 0 && kvh == 0 && tid == 0, n, T);
+  // a tile works when one of its rows belongs to a tree row
+  const bool has_a = q0 < n * g, has_b = q0 + BM < n * g;
+  const int nct = (T + BN - 1) / BN;
+  const int ntt = (n + BN - 1) / BN;
+  const int t_lo = min(split * p.steps_per_split, nct + ntt);
+  const int t_hi = min(t_lo + p.steps_per_split, nct + ntt);
+  const int ntiles = has_a ? t_hi - t_lo : 0;
+
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sh->tmem_base;
+
+  if (wg == 0) {
+    regs_dec<48>();
+    if (warp == 1 && lane == 0 && ntiles > 0) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t kIdQK = idesc_f16(false), kIdPV = idesc_f16(true);
+      const int nt = has_b ? 2 : 1;
+      const uint32_t q_lo = desc_lo(sQ, 16), k_lo = desc_lo(sKV, 16), v_lo = desc_lo(sKV, kHalfTile);
+      auto qk = [&](int x, int i) {  // S_x = Q_x K_i^T
+        const uint32_t q = q_lo + x * (kTile >> 4), k = k_lo + ((2 * i) & 3) * (kTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (uint32_t)((kk >> 2) * kHalfTile + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + kColS + 128 * x, desc_of(q + off), desc_of(k + off), kIdQK, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&sh->s_full[x]);
+      };
+      auto pv = [&](int x, int i) {  // O_x += P_x V_i, P_x in the first half of S_x
+        const uint32_t v = v_lo + ((2 * i + 1) & 3) * (kTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          mma_ts(tmem + kColO + 128 * x, tmem + kColS + 128 * x + kk * 8, desc_of(v + kk * (2048 >> 4)), kIdPV,
+                 (i > 0 || kk > 0) ? 1u : 0u);
+      };
+      bool go = wait(&sh->q_full, 0, sh) && wait(&sh->kv_full[0], 0, sh);
+      if (go) {
+        fence_after();
+        for (int x = 0; x < nt; ++x) qk(x, 0);
+        mma_commit(&sh->kv_empty[0]);  // K_0
+      }
+      for (int i = 0; go && i < ntiles; ++i) {
+        const int vs = (2 * i + 1) & 3, ks1 = (2 * i + 2) & 3;
+        const bool next = i + 1 < ntiles;
+        if (!wait(&sh->kv_full[vs], (uint32_t)(i >> 1) & 1u, sh)) break;
+        for (int x = 0; x < nt; ++x) {
+          if (!wait(&sh->p_full[x], (uint32_t)i & 1u, sh) ||
+              (next && x == 0 && !wait(&sh->kv_full[ks1], (uint32_t)((i + 1) >> 1) & 1u, sh))) {
+            go = false;
+            break;
+          }
+          fence_after();
+          pv(x, i);
+          if (next) qk(x, i + 1);
+        }
+        if (!go) break;
+        mma_commit(&sh->kv_empty[vs]);             // V_i: every PV of step i issued
+        if (next) mma_commit(&sh->kv_empty[ks1]);  // K_{i+1}
+      }
+      if (go) mma_commit(&sh->o_full);
+      if (*(volatile int*)&sh->abort) {
+        int keep_going = 0;
+        mma_commit(&sh->drain);
+        mbar_wait_bounded(&sh->drain, 0u, &keep_going, kDrainCycles);
+      }
+    }
+  } else if (wg == 3) {
+    // ------------------------------------------------------------ converter
+    regs_dec<112>();
+    const int cw = warp & 3, ct = tid & 127;
+    const int tok = ct >> 3, ch = ct & 7;     // of a group of 16 tokens; 16 elements
+    const int64_t stride = (int64_t)p.c.hkv * D;
+    const int64_t lane_off = (int64_t)kvh * D + tok * stride + ch * 16;
+    const int nctx = min(max(nct - t_lo, 0), ntiles);  // context tiles of this CTA
+    // places and exponents of the groups of 4 tiles, a group a lane
+    int rows = -1, ek = 0, ev = 0;
+    auto look_up = [&](int i) {  // of tiles i .. i + 3
+      rows = -1;
+      const int64_t pos = ((int64_t)(t_lo + i) * kGroups + lane) * kGroup;
+      if (i + (lane >> 3) < nctx && pos < T) {
+        const Q8Place at = q8_place(p.c, b, pos);
+        if (at.row < 0) {
+          if (cw == 0) raise_status(p.status, DDT_ERR_INVALID_ARG);
+        } else {
+          rows = (int)at.row;
+          ek = p.c.ke[at.blk * p.c.hkv + kvh];
+          ev = p.c.ve[at.blk * p.c.hkv + kvh];
+        }
+      }
+    };
+    uint4 x[kGroups];
+    auto load = [&](int i, int gq, const uint8_t* base) {  // group gq of tile i
+      const int r = __shfl_sync(0xFFFFFFFFu, rows, (i & 3) * 8 + gq);
+      x[gq] = r >= 0 ? ld_stream_v4(base + r * stride + lane_off) : make_uint4(0, 0, 0, 0);
+    };
+    // two 16-byte chunks of f16; lanes of the two slices take them in turn (no bank conflicts)
+    const int flip = ch >> 2;
+    auto store = [&](unsigned char* dst, int r, uint4 lo, uint4 hi) {
+      const uint4 a = flip ? hi : lo, c = flip ? lo : hi;
+      *(uint4*)(dst + tile_at(r, 2 * ch + flip)) = a;
+      *(uint4*)(dst + tile_at(r, 2 * ch + 1 - flip)) = c;
+    };
+    auto done = [&](int c) {  // load c is in its slot
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->kv_full[c & 3]);
+    };
+    bool go = true;
+    if (nctx > 0) {
+      look_up(0);
+#pragma unroll
+      for (int gq = 0; gq < kGroups; ++gq) load(0, gq, p.c.kc);
+    }
+    for (int i = 0; go && i < nctx; ++i) {
+      const int e_k = __shfl_sync(0xFFFFFFFFu, ek, (i & 3) * 8 + (lane & 7));
+      const int e_v = __shfl_sync(0xFFFFFFFFu, ev, (i & 3) * 8 + (lane & 7));
+      const int r = __shfl_sync(0xFFFFFFFFu, rows, (i & 3) * 8 + (lane & 7));
+      if (cw == 0 && lane < kGroups)
+        sh->scales[i & 3][lane] =
+            make_float2(q8_scale(e_k), r < 0 ? -INFINITY
+                                             : e_v == DDT_Q8_EXP_NAN ? __int_as_float(0x7FC00000)
+                                                                     : (float)(q8_exp(e_v) + kCodeShift));
+      __syncwarp();
+      if (cw == 0 && lane == 0) mbar_arrive(&sh->sc_full[i & 3]);
+#pragma unroll
+      for (int kind = 0; kind < 2; ++kind) {
+        const int c = 2 * i + kind;
+        go = go && __all_sync(0xFFFFFFFFu, wait(&sh->kv_empty[c & 3], ((uint32_t)(c >> 2) & 1u) ^ 1u, sh));
+        if (!go) break;
+        // what follows into the registers: V of this tile, then K of the next
+        const int ni = kind ? i + 1 : i;
+        if (kind && ni < nctx && (ni & 3) == 0) look_up(ni);
+        const uint8_t* base = kind ? p.c.kc : p.c.vc;
+        unsigned char* dst = sKV + (c & 3) * kTile;
+#pragma unroll
+        for (int gq = 0; gq < kGroups; ++gq) {
+          const uint4 v = x[gq];
+          if (ni < nctx) load(ni, gq, base);
+          store(dst, gq * kGroup + tok, make_uint4(codes_lo(v.x), codes_hi(v.x), codes_lo(v.y), codes_hi(v.y)),
+                make_uint4(codes_lo(v.z), codes_hi(v.z), codes_lo(v.w), codes_hi(v.w)));
+        }
+        done(c);
+      }
+    }
+    for (int i = nctx; i < ntiles; ++i) {
+      // ---- a tile of tree rows: bf16 to f16 under a power of two per group
+      const int row0 = (t_lo + i - nct) * BN;
+#pragma unroll 1
+      for (int kind = 0; kind < 2; ++kind) {
+        const int c = 2 * i + kind;
+        go = all_of_converter(go);  // (the four warps leave together; amax may be written again)
+        if (!go) break;
+        const uint16_t* src = (kind ? p.vt : p.kt) + (((int64_t)b * p.n_max + row0) * p.c.hkv + kvh) * D + ch * 16;
+        // largest finite magnitudes, a group at a time
+#pragma unroll 1
+        for (int gq = 0; gq < kGroups; ++gq) {
+          const int r = gq * kGroup + tok;
+          uint32_t m = 0;
+          bool odd = false;
+          if (row0 + r < n) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint4 v = __ldg((const uint4*)(src + r * stride) + h);
+              m = max_finite_bf16(max_finite_bf16(max_finite_bf16(max_finite_bf16(m, v.x), v.y), v.z), v.w);
+              odd |= max(max(max_bf16(v.x), max_bf16(v.y)), max(max_bf16(v.z), max_bf16(v.w))) >= 0x7F80u;
+            }
+            if (odd && kind) atomicOr(&sh->odd[(row0 + r) >> 5], 1u << ((row0 + r) & 31));
+          }
+          m = __reduce_max_sync(0xFFFFFFFFu, m);
+          if (lane == 0) sh->amax[cw][gq] = m;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const int gl = lane & 7;
+        const uint32_t m = max(max(sh->amax[0][gl], sh->amax[1][gl]), max(sh->amax[2][gl], sh->amax[3][gl]));
+        const int e = min(max(f16_exponent(m, kTreeTop), DDT_Q8_EXP_MIN), DDT_Q8_EXP_MAX);
+        if (cw == 0 && lane < kGroups) {
+          if (kind == 0)
+            sh->scales[i & 3][lane].x = pow2i(e);
+          else
+            sh->scales[i & 3][lane].y = (float)e;
+        }
+        __syncwarp();
+        if (kind && cw == 0 && lane == 0) mbar_arrive(&sh->sc_full[i & 3]);
+        go = __all_sync(0xFFFFFFFFu, wait(&sh->kv_empty[c & 3], ((uint32_t)(c >> 2) & 1u) ^ 1u, sh));
+        if (!go) continue;
+        unsigned char* dst = sKV + (c & 3) * kTile;
+#pragma unroll 1
+        for (int gq = 0; gq < kGroups; ++gq) {
+          const int r = gq * kGroup + tok;
+          const float inv = pow2i(-__shfl_sync(0xFFFFFFFFu, e, gq));
+          uint4 f[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row0 + r < n) v = __ldg((const uint4*)(src + r * stride) + h);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (kind) {  // non-finite V elements go to their rows at the end, and to no others
+                if ((w[q] & 0x7F80u) == 0x7F80u) w[q] &= 0xFFFF0000u;
+                if ((w[q] & 0x7F800000u) == 0x7F800000u) w[q] &= 0x0000FFFFu;
+              }
+              w[q] = bf16x2_to_f16x2(w[q], inv);
+            }
+            f[h] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          store(dst, r, f[0], f[1]);
+        }
+        done(c);
+      }
+      if (!go) break;
+    }
+    asm volatile("bar.arrive 2, 384;" ::: "memory");
+  } else {
+    // ------------------------------------------------------------ softmax
+    regs_inc<176>();
+    // ---- Q as f16 under a power of two per row: a row per softmax thread
+    const int t = wg - 1;                            // softmax tile
+    const int row = (warp & 3) * 32 + lane;
+    const int qr = q0 + t * BM + row, jq = qr / g;
+    const bool tile_live = t == 0 ? has_a : has_b;
+    const bool row_valid = tile_live && qr < n * g;
+    const int64_t out_row = ((int64_t)b * p.n_max + jq) * p.hq + kvh * g + qr % g;
+    float mul = 0.f;
+    if (tile_live && ntiles > 0) {
+      const uint4* src = (const uint4*)(p.q + out_row * D);
+      uint32_t m = 0;
+      if (row_valid) {
+  #pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint4 v = __ldg(src + i);
+          m = max_finite_bf16(max_finite_bf16(max_finite_bf16(max_finite_bf16(m, v.x), v.y), v.z), v.w);
+        }
+      }
+      const int e = m ? max(f16_exponent(m, 14), -126) : 0;
+      const float inv = pow2i(-e);
+      mul = p.scale_log2 * pow2i(e);
+      unsigned char* dst = sQ + t * kTile;
+  #pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row_valid) v = __ldg(src + i);
+        *(uint4*)(dst + tile_at(row, i)) = make_uint4(bf16x2_to_f16x2(v.x, inv), bf16x2_to_f16x2(v.y, inv),
+                                                      bf16x2_to_f16x2(v.z, inv), bf16x2_to_f16x2(v.w, inv));
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->q_full);
+    float m_ref = -INFINITY, l = 0.f;
+    bool ok = true;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_col = lane_base + kColS + 128 * t, o_col = lane_base + kColO + 128 * t;
+    const uint32_t* mrow = p.mask + ((int64_t)b * p.n_max + (row_valid ? jq : 0)) * p.W;
+    for (int i = 0; tile_live && i < ntiles; ++i) {
+      const int ti = t_lo + i;
+      const bool tree = ti >= nct;
+      const int base = (tree ? ti - nct : ti) * BN;
+      const int cnt = min(BN, (tree ? n : T) - base);
+      ok = __all_sync(0xFFFFFFFFu, wait(&sh->sc_full[i & 3], (uint32_t)(i >> 2) & 1u, sh) &&
+                                       wait(&sh->s_full[t], (uint32_t)i & 1u, sh));
+      if (!ok) break;
+      fence_after();
+      uint32_t r[BN];
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_col + 32 * c, r + 32 * c);
+      tmem_ld_wait();
+      // t_j = s_j + V exponent, two scores at a time
+#pragma unroll
+      for (int q = 0; q < kGroups; ++q) {
+        const float2 sc = sh->scales[i & 3][q];
+        const float f = mul * sc.x;
+        const uint64_t f2 = pack2(f, f), e2 = pack2(sc.y, sc.y);
+#pragma unroll
+        for (int e = 0; e < kGroup; e += 2) {
+          float a, c;
+          unpack2(ffma2(pack2(__uint_as_float(r[q * 16 + e]), __uint_as_float(r[q * 16 + e + 1])), f2, e2), a, c);
+          r[q * 16 + e] = __float_as_uint(a);
+          r[q * 16 + e + 1] = __float_as_uint(c);
+        }
+      }
+      if (tree || cnt < BN) {
+#pragma unroll
+        for (int w = 0; w < BN / 32; ++w) {
+          const int have = cnt - 32 * w;
+          uint32_t bits = have >= 32 ? 0xFFFFFFFFu : (have > 0 ? (1u << have) - 1u : 0u);
+          if (tree) bits = row_valid && (base >> 5) + w < p.W ? bits & __ldg(mrow + (base >> 5) + w) : 0u;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!((bits >> e) & 1u)) r[32 * w + e] = 0xFF800000u;  // -inf
+        }
+      }
+      float m4[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m4[e] = __uint_as_float(r[e]);
+#pragma unroll
+      for (int e = 4; e < BN; e += 2)
+        m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+      const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      float alpha = 1.f;
+      const bool move = top > m_ref + (kSlack + kHead);
+      if (move) {
+        alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - (top - kHead));
+        m_ref = top - kHead;
+        l *= alpha;
+      }
+      const float m = m_ref == -INFINITY ? 0.f : m_ref;
+      const uint64_t nm2 = pack2(-m, -m);
+      // P = 2^(t - m) as f16 pairs over the scores, its sum weighted by 2^-(V exponent)
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint64_t s2[2] = {0ull, 0ull};
+#pragma unroll
+          for (int e = 0; e < kGroup; e += 2) {
+            const int at = 32 * c + 16 * q + e;
+            float a, z;
+            unpack2(fadd2(pack2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), nm2), a, z);
+            a = ex2(a);
+            z = ex2(z);
+            s2[(e >> 1) & 1] = fadd2(s2[(e >> 1) & 1], pack2(a, z));
+            pk[8 * q + (e >> 1)] = f32x2_to_f16x2(a, z);
+          }
+          float a, z;
+          unpack2(fadd2(s2[0], s2[1]), a, z);
+          // (a group that is not there has weights 0 and must not meet 2^inf)
+          l = fmaf(a + z, ex2(fminf(-sh->scales[i & 3][2 * c + q].y, 126.f)), l);
+        }
+        tmem_st16(s_col + 16 * c, pk);
+      }
+      // O_t holds PV_t(i-1) (complete: the commit behind s_full covers it)
+      if (i > 0 && __any_sync(0xFFFFFFFFu, move)) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_col + 32 * c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st32(o_col + 32 * c, o);
+        }
+      }
+      tmem_st_wait();
+      fence_before();
+      mbar_arrive(&sh->p_full[t]);
+    }
+    if (tile_live && ok && ntiles > 0) ok = __all_sync(0xFFFFFFFFu, wait(&sh->o_full, 0, sh));
+    asm volatile("bar.sync 2, 384;" ::: "memory");  // the converter's marks in sh->odd are complete
+    fence_after();
+
+    // ---- epilogue: O rows to the output or to a split's partial
+    const bool final_out = p.nsplit == 1;
+    const bool has = ok && row_valid && ntiles > 0 && l != 0.f;  // (NaN counts as a sum)
+    const float inv = has ? 1.f / l : 0.f;
+    const bool writes = final_out ? qr < R : row_valid;
+    const int64_t prow = ((int64_t)grp * p.nsplit + split) * R + qr;
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t o[32];
+      if (tile_live && ntiles > 0) {  // (warp-collective)
+        tmem_ld32(o_col + 32 * c, o);
+        tmem_ld_wait();
+      }
+      if (!has) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
+      } else if (t_hi > nct) {
+        // non-finite V elements of the tree rows that this row sees, in this CTA's tiles
+        const int w_lo = max(t_lo - nct, 0) * 4, w_hi = min((t_hi - nct) * 4, p.W);
+#pragma unroll 1
+        for (int w = w_lo; w < w_hi; ++w) {
+          uint32_t bits = sh->odd[w];
+          if (bits) bits &= __ldg(p.mask + ((int64_t)b * p.n_max + jq) * p.W + w);
+          while (bits) {
+            const int tr = w * 32 + __ffs(bits) - 1;
+            bits &= bits - 1;
+            const uint16_t* v = p.vt + (((int64_t)b * p.n_max + tr) * p.c.hkv + kvh) * D + 32 * c;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const uint16_t z = v[e];
+              if ((z & 0x7F80u) == 0x7F80u) o[e] = __float_as_uint(__uint_as_float(o[e]) + bf16_to_f32(z));
+            }
+          }
+        }
+      }
+      if (!writes) {
+      } else if (final_out) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          pk[e] = f32x2_to_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+        uint4* dst = (uint4*)(p.out + out_row * D + 32 * c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+      } else {
+        float4* dst = (float4*)(p.part_o + prow * D + 32 * c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                               __uint_as_float(o[4 * e + 3]));
+      }
+    }
+    // (a row of NaN scores alone has no reference: any number carries its NaN on)
+    if (l != l) m_ref = 0.f;
+    if (writes && final_out) {
+      if (p.lse_out) p.lse_out[out_row] = has ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+    } else if (writes) {
+      p.part_ml[prow] = has ? make_float2(m_ref, l) : make_float2(-INFINITY, 0.f);
+    }
+  }
+  pdl_trigger();
+  fence_before();
+  __syncthreads();
+  if (tid == 0 && sh->abort) raise_status(p.status, DDT_ERR_TIMEOUT);
+  if (warp == 0) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_q8_wide(const AttnQ8Params& p, int pairs, cudaStream_t stream) {
+  const size_t smem = 1024 + (size_t)(2 + kSlots) * kTile + sizeof(Shared);
+  const cudaError_t e = ensure_smem_attr((const void*)attn_q8_wide_kernel, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_q8_wide_kernel, dim3(pairs, p.nsplit, p.batch * p.c.hkv), dim3(kThreads), smem, stream, 0, p);
+}
+
+}  // namespace ddt
