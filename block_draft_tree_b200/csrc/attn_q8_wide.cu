@@ -21,7 +21,7 @@
 //   * warpgroups 1 and 2 are the softmax of A and B, a row per thread: the 128
 //     scores in registers, the context bound and the ancestor bitset as masks,
 //     P over the scores' columns, O rescaled only when the reference moves.
-// Registers go to where they are needed by setmaxnreg: 48 + 2 x 176 + 112.
+// Registers go to where they are needed by setmaxnreg: 40 + 2 x 160 + 152.
 // KV splits write (O, m, l) partials that attn_q8_combine merges.  Every wait
 // is bounded; one that gives up raises DDT_ERR_TIMEOUT.
 #include "attn_q8.cuh"
@@ -54,7 +54,7 @@ struct __align__(16) Shared {
   uint32_t tmem_base;
   int abort;
   float2 scales[4][kGroups];  // (what a K product counts for, V exponent)
-  uint32_t amax[4][kGroups];  // converter warps' largest magnitudes of a tree tile
+  uint32_t amax[2][kGroups];  // largest magnitudes of a tree tile's groups, from two warps each
   uint32_t odd[32];           // tree rows with a non-finite V element
 };
 
@@ -72,6 +72,15 @@ __device__ __forceinline__ void regs_dec() {
 // kind::f16, f16 x f16 -> f32, M = 128, N = 128, A K-major; B K-major or MN-major.
 constexpr uint32_t idesc_f16(bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+}
+// One lane of a converged warp.  The issuer's branch is on elect.sync and not
+// on a lane number: the compiler then keeps the operands of the MMAs in
+// uniform registers (measured: 65 cycles an MMA of 128 x 128 x 16, which is
+// the tensor pipe's rate, against 108 to 156 under `lane == 0`).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 // A shared-memory descriptor from its varying low word (128-byte swizzle, 1024
 // bytes between groups of 8 rows), so that the issuer's registers hold one word each.
@@ -157,8 +166,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
   const uint32_t tmem = sh->tmem_base;
 
   if (wg == 0) {
-    regs_dec<48>();
-    if (warp == 1 && lane == 0 && ntiles > 0) {
+    regs_dec<40>();
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    if (warp == 1 && ntiles > 0 && elect_one()) {
       // ------------------------------------------------------------ MMA issuer
       constexpr uint32_t kIdQK = idesc_f16(false), kIdPV = idesc_f16(true);
       const int nt = has_b ? 2 : 1;
@@ -168,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (uint32_t)((kk >> 2) * kHalfTile + (kk & 3) * 32) >> 4;
-          mma_ss(tmem + kColS + 128 * x, desc_of(q + off), desc_of(k + off), kIdQK, kk > 0 ? 1u : 0u);
+          mma_ss(tm + kColS + 128 * x, desc_of(q + off), desc_of(k + off), kIdQK, kk > 0 ? 1u : 0u);
         }
         mma_commit(&sh->s_full[x]);
       };
@@ -176,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
         const uint32_t v = v_lo + ((2 * i + 1) & 3) * (kTile >> 4);
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts(tmem + kColO + 128 * x, tmem + kColS + 128 * x + kk * 8, desc_of(v + kk * (2048 >> 4)), kIdPV,
+          mma_ts(tm + kColO + 128 * x, tm + kColS + 128 * x + kk * 8, desc_of(v + kk * (2048 >> 4)), kIdPV,
                  (i > 0 || kk > 0) ? 1u : 0u);
       };
       bool go = wait(&sh->q_full, 0, sh) && wait(&sh->kv_full[0], 0, sh);
@@ -212,39 +222,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     }
   } else if (wg == 3) {
     // ------------------------------------------------------------ converter
-    regs_dec<112>();
+    regs_inc<152>();
     const int cw = warp & 3, ct = tid & 127;
-    const int tok = ct >> 3, ch = ct & 7;     // of a group of 16 tokens; 16 elements
-    const int64_t stride = (int64_t)p.c.hkv * D;
-    const int64_t lane_off = (int64_t)kvh * D + tok * stride + ch * 16;
+    const int tok = ct >> 2, c4 = ct & 3;  // of 32 tokens; 16 elements of a 64-wide slice
+    const uint32_t stride = (uint32_t)p.c.hkv * D;
     const int nctx = min(max(nct - t_lo, 0), ntiles);  // context tiles of this CTA
-    // places and exponents of the groups of 4 tiles, a group a lane
-    int rows = -1, ek = 0, ev = 0;
-    auto look_up = [&](int i) {  // of tiles i .. i + 3
-      rows = -1;
+    // places and exponents of the 16-token groups of 4 tiles, a group a lane; a
+    // group that is not there reads row 0 and weighs nothing
+    struct LookUp {
+      int row, ek, ev;
+      bool there;
+    };
+    auto look_up = [&](int i) -> LookUp {  // of tiles i .. i + 3
+      LookUp u{0, 0, 0, false};
       const int64_t pos = ((int64_t)(t_lo + i) * kGroups + lane) * kGroup;
       if (i + (lane >> 3) < nctx && pos < T) {
         const Q8Place at = q8_place(p.c, b, pos);
         if (at.row < 0) {
           if (cw == 0) raise_status(p.status, DDT_ERR_INVALID_ARG);
         } else {
-          rows = (int)at.row;
-          ek = p.c.ke[at.blk * p.c.hkv + kvh];
-          ev = p.c.ve[at.blk * p.c.hkv + kvh];
+          u.there = true;
+          u.row = (int)at.row;
+          u.ek = p.c.ke[at.blk * p.c.hkv + kvh];
+          u.ev = p.c.ve[at.blk * p.c.hkv + kvh];
         }
       }
+      return u;
     };
-    uint4 x[kGroups];
-    auto load = [&](int i, int gq, const uint8_t* base) {  // group gq of tile i
-      const int r = __shfl_sync(0xFFFFFFFFu, rows, (i & 3) * 8 + gq);
-      x[gq] = r >= 0 ? ld_stream_v4(base + r * stride + lane_off) : make_uint4(0, 0, 0, 0);
+    // K and V codes of the next tile to convert: pass q holds slice q & 1 of
+    // tokens 32 (q / 2) + tok, of group 2 (q / 2) + (warp >= 2)
+    uint4 xk[8], xv[8];
+    const int64_t lane_off = (int64_t)kvh * D + (tok & 15) * (int64_t)stride + c4 * 16;
+    const uint8_t *k_lane = p.c.kc + lane_off, *v_lane = p.c.vc + lane_off;
+    auto load = [&](const LookUp& u, int i, int q, const uint8_t* base) {
+      const int r = __shfl_sync(0xFFFFFFFFu, u.row, (i & 3) * 8 + (q >> 1) * 2 + (cw >> 1));
+      return ld_stream_v4(base + (uint64_t)(uint32_t)r * stride + (q & 1) * 64);
     };
-    // two 16-byte chunks of f16; lanes of the two slices take them in turn (no bank conflicts)
-    const int flip = ch >> 2;
-    auto store = [&](unsigned char* dst, int r, uint4 lo, uint4 hi) {
-      const uint4 a = flip ? hi : lo, c = flip ? lo : hi;
-      *(uint4*)(dst + tile_at(r, 2 * ch + flip)) = a;
-      *(uint4*)(dst + tile_at(r, 2 * ch + 1 - flip)) = c;
+    // 16 elements as f16 to their two chunks of row r (of rows of two parities
+    // a quarter warp writes, the swizzle gives eight different banks)
+    auto store = [&](unsigned char* dst, int r, int slice, uint4 lo, uint4 hi) {
+      *(uint4*)(dst + tile_at(r, slice * 8 + 2 * c4)) = lo;
+      *(uint4*)(dst + tile_at(r, slice * 8 + 2 * c4 + 1)) = hi;
     };
     auto done = [&](int c) {  // load c is in its slot
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -252,37 +270,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
       if (lane == 0) mbar_arrive(&sh->kv_full[c & 3]);
     };
     bool go = true;
+    LookUp now = {}, then = {};
     if (nctx > 0) {
-      look_up(0);
+      now = look_up(0);
 #pragma unroll
-      for (int gq = 0; gq < kGroups; ++gq) load(0, gq, p.c.kc);
+      for (int q = 0; q < 8; ++q) xk[q] = load(now, 0, q, k_lane);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) xv[q] = load(now, 0, q, v_lane);
     }
     for (int i = 0; go && i < nctx; ++i) {
-      const int e_k = __shfl_sync(0xFFFFFFFFu, ek, (i & 3) * 8 + (lane & 7));
-      const int e_v = __shfl_sync(0xFFFFFFFFu, ev, (i & 3) * 8 + (lane & 7));
-      const int r = __shfl_sync(0xFFFFFFFFu, rows, (i & 3) * 8 + (lane & 7));
-      if (cw == 0 && lane < kGroups)
-        sh->scales[i & 3][lane] =
-            make_float2(q8_scale(e_k), r < 0 ? -INFINITY
-                                             : e_v == DDT_Q8_EXP_NAN ? __int_as_float(0x7FC00000)
-                                                                     : (float)(q8_exp(e_v) + kCodeShift));
-      __syncwarp();
-      if (cw == 0 && lane == 0) mbar_arrive(&sh->sc_full[i & 3]);
+      {
+        const int src = (i & 3) * 8 + (lane & 7);
+        const int ek = __shfl_sync(0xFFFFFFFFu, now.ek, src), ev = __shfl_sync(0xFFFFFFFFu, now.ev, src);
+        const bool there = __shfl_sync(0xFFFFFFFFu, (int)now.there, src);
+        if (cw == 0 && lane < kGroups)
+          sh->scales[i & 3][lane] =
+              make_float2(q8_scale(ek), !there ? -INFINITY
+                                               : ev == DDT_Q8_EXP_NAN ? __int_as_float(0x7FC00000)
+                                                                      : (float)(q8_exp(ev) + kCodeShift));
+        __syncwarp();
+        if (cw == 0 && lane == 0) mbar_arrive(&sh->sc_full[i & 3]);
+      }
+      if ((i & 3) == 1) then = look_up((i & ~3) + 4);
+      if ((i & 3) == 3) now = then;  // from here on for tile i + 1
 #pragma unroll
       for (int kind = 0; kind < 2; ++kind) {
         const int c = 2 * i + kind;
         go = go && __all_sync(0xFFFFFFFFu, wait(&sh->kv_empty[c & 3], ((uint32_t)(c >> 2) & 1u) ^ 1u, sh));
         if (!go) break;
-        // what follows into the registers: V of this tile, then K of the next
-        const int ni = kind ? i + 1 : i;
-        if (kind && ni < nctx && (ni & 3) == 0) look_up(ni);
-        const uint8_t* base = kind ? p.c.kc : p.c.vc;
         unsigned char* dst = sKV + (c & 3) * kTile;
 #pragma unroll
-        for (int gq = 0; gq < kGroups; ++gq) {
-          const uint4 v = x[gq];
-          if (ni < nctx) load(ni, gq, base);
-          store(dst, gq * kGroup + tok, make_uint4(codes_lo(v.x), codes_hi(v.x), codes_lo(v.y), codes_hi(v.y)),
+        for (int q = 0; q < 8; ++q) {
+          const uint4 v = kind ? xv[q] : xk[q];
+          if (i + 1 < nctx) (kind ? xv : xk)[q] = load(now, i + 1, q, kind ? v_lane : k_lane);
+          store(dst, (q >> 1) * 32 + tok, q & 1,
+                make_uint4(codes_lo(v.x), codes_hi(v.x), codes_lo(v.y), codes_hi(v.y)),
                 make_uint4(codes_lo(v.z), codes_hi(v.z), codes_lo(v.w), codes_hi(v.w)));
         }
         done(c);
@@ -296,28 +318,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
         const int c = 2 * i + kind;
         go = all_of_converter(go);  // (the four warps leave together; amax may be written again)
         if (!go) break;
-        const uint16_t* src = (kind ? p.vt : p.kt) + (((int64_t)b * p.n_max + row0) * p.c.hkv + kvh) * D + ch * 16;
-        // largest finite magnitudes, a group at a time
+        const uint16_t* src = (kind ? p.vt : p.kt) + (((int64_t)b * p.n_max + row0) * p.c.hkv + kvh) * D + c4 * 16;
+        // largest finite magnitudes, a group (half the warps) at a time
 #pragma unroll 1
-        for (int gq = 0; gq < kGroups; ++gq) {
-          const int r = gq * kGroup + tok;
+        for (int q = 0; q < 4; ++q) {
+          const int r = q * 32 + tok;
           uint32_t m = 0;
           bool odd = false;
           if (row0 + r < n) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 v = __ldg((const uint4*)(src + r * stride) + h);
+            for (int h = 0; h < 4; ++h) {
+              const uint4 v = __ldg((const uint4*)(src + (int64_t)r * stride + (h >> 1) * 64) + (h & 1));
               m = max_finite_bf16(max_finite_bf16(max_finite_bf16(max_finite_bf16(m, v.x), v.y), v.z), v.w);
               odd |= max(max(max_bf16(v.x), max_bf16(v.y)), max(max_bf16(v.z), max_bf16(v.w))) >= 0x7F80u;
             }
             if (odd && kind) atomicOr(&sh->odd[(row0 + r) >> 5], 1u << ((row0 + r) & 31));
           }
           m = __reduce_max_sync(0xFFFFFFFFu, m);
-          if (lane == 0) sh->amax[cw][gq] = m;
+          if (lane == 0) sh->amax[cw & 1][2 * q + (cw >> 1)] = m;
         }
         asm volatile("bar.sync 1, 128;" ::: "memory");
-        const int gl = lane & 7;
-        const uint32_t m = max(max(sh->amax[0][gl], sh->amax[1][gl]), max(sh->amax[2][gl], sh->amax[3][gl]));
+        const uint32_t m = max(sh->amax[0][lane & 7], sh->amax[1][lane & 7]);
         const int e = min(max(f16_exponent(m, kTreeTop), DDT_Q8_EXP_MIN), DDT_Q8_EXP_MAX);
         if (cw == 0 && lane < kGroups) {
           if (kind == 0)
@@ -331,26 +352,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
         if (!go) continue;
         unsigned char* dst = sKV + (c & 3) * kTile;
 #pragma unroll 1
-        for (int gq = 0; gq < kGroups; ++gq) {
-          const int r = gq * kGroup + tok;
-          const float inv = pow2i(-__shfl_sync(0xFFFFFFFFu, e, gq));
+        for (int q = 0; q < 8; ++q) {
+          const int r = (q >> 1) * 32 + tok;
+          const float inv = pow2i(-__shfl_sync(0xFFFFFFFFu, e, (q >> 1) * 2 + (cw >> 1)));
           uint4 f[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint4 v = make_uint4(0, 0, 0, 0);
-            if (row0 + r < n) v = __ldg((const uint4*)(src + r * stride) + h);
+            if (row0 + r < n) v = __ldg((const uint4*)(src + (int64_t)r * stride + (q & 1) * 64) + h);
             uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int x = 0; x < 4; ++x) {
               if (kind) {  // non-finite V elements go to their rows at the end, and to no others
-                if ((w[q] & 0x7F80u) == 0x7F80u) w[q] &= 0xFFFF0000u;
-                if ((w[q] & 0x7F800000u) == 0x7F800000u) w[q] &= 0x0000FFFFu;
+                if ((w[x] & 0x7F80u) == 0x7F80u) w[x] &= 0xFFFF0000u;
+                if ((w[x] & 0x7F800000u) == 0x7F800000u) w[x] &= 0x0000FFFFu;
               }
-              w[q] = bf16x2_to_f16x2(w[q], inv);
+              w[x] = bf16x2_to_f16x2(w[x], inv);
             }
             f[h] = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          store(dst, r, f[0], f[1]);
+          store(dst, r, q & 1, f[0], f[1]);
         }
         done(c);
       }
@@ -359,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     asm volatile("bar.arrive 2, 384;" ::: "memory");
   } else {
     // ------------------------------------------------------------ softmax
-    regs_inc<176>();
+    regs_inc<160>();
     // ---- Q as f16 under a power of two per row: a row per softmax thread
     const int t = wg - 1;                            // softmax tile
     const int row = (warp & 3) * 32 + lane;
