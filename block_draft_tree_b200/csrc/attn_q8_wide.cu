@@ -319,21 +319,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
         go = all_of_converter(go);  // (the four warps leave together; amax may be written again)
         if (!go) break;
         const uint16_t* src = (kind ? p.vt : p.kt) + (((int64_t)b * p.n_max + row0) * p.c.hkv + kvh) * D + c4 * 16;
-        // largest finite magnitudes, a group (half the warps) at a time
-#pragma unroll 1
+        // the tile's rows in registers: pass q as for the codes
+        uint4 x[8][2];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int r = (q >> 1) * 32 + tok;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            x[q][h] = make_uint4(0, 0, 0, 0);
+            if (row0 + r < n) x[q][h] = __ldg((const uint4*)(src + (int64_t)r * stride + (q & 1) * 64) + h);
+          }
+        }
+        // largest finite magnitudes, a group from two warps
+#pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int r = q * 32 + tok;
           uint32_t m = 0;
           bool odd = false;
-          if (row0 + r < n) {
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const uint4 v = __ldg((const uint4*)(src + (int64_t)r * stride + (h >> 1) * 64) + (h & 1));
-              m = max_finite_bf16(max_finite_bf16(max_finite_bf16(max_finite_bf16(m, v.x), v.y), v.z), v.w);
-              odd |= max(max(max_bf16(v.x), max_bf16(v.y)), max(max_bf16(v.z), max_bf16(v.w))) >= 0x7F80u;
-            }
-            if (odd && kind) atomicOr(&sh->odd[(row0 + r) >> 5], 1u << ((row0 + r) & 31));
+          for (int h = 0; h < 4; ++h) {
+            const uint4 v = x[2 * q + (h >> 1)][h & 1];
+            m = max_finite_bf16(max_finite_bf16(max_finite_bf16(max_finite_bf16(m, v.x), v.y), v.z), v.w);
+            odd |= max(max(max_bf16(v.x), max_bf16(v.y)), max(max_bf16(v.z), max_bf16(v.w))) >= 0x7F80u;
           }
+          if (odd && kind) atomicOr(&sh->odd[(row0 + q * 32 + tok) >> 5], 1u << ((row0 + q * 32 + tok) & 31));
           m = __reduce_max_sync(0xFFFFFFFFu, m);
           if (lane == 0) sh->amax[cw & 1][2 * q + (cw >> 1)] = m;
         }
@@ -351,23 +359,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
         go = __all_sync(0xFFFFFFFFu, wait(&sh->kv_empty[c & 3], ((uint32_t)(c >> 2) & 1u) ^ 1u, sh));
         if (!go) continue;
         unsigned char* dst = sKV + (c & 3) * kTile;
-#pragma unroll 1
+#pragma unroll
         for (int q = 0; q < 8; ++q) {
           const int r = (q >> 1) * 32 + tok;
           const float inv = pow2i(-__shfl_sync(0xFFFFFFFFu, e, (q >> 1) * 2 + (cw >> 1)));
           uint4 f[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row0 + r < n) v = __ldg((const uint4*)(src + (int64_t)r * stride + (q & 1) * 64) + h);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t w[4] = {x[q][h].x, x[q][h].y, x[q][h].z, x[q][h].w};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int z = 0; z < 4; ++z) {
               if (kind) {  // non-finite V elements go to their rows at the end, and to no others
-                if ((w[x] & 0x7F80u) == 0x7F80u) w[x] &= 0xFFFF0000u;
-                if ((w[x] & 0x7F800000u) == 0x7F800000u) w[x] &= 0x0000FFFFu;
+                if ((w[z] & 0x7F80u) == 0x7F80u) w[z] &= 0xFFFF0000u;
+                if ((w[z] & 0x7F800000u) == 0x7F800000u) w[z] &= 0x0000FFFFu;
               }
-              w[x] = bf16x2_to_f16x2(w[x], inv);
+              w[z] = bf16x2_to_f16x2(w[z], inv);
             }
             f[h] = make_uint4(w[0], w[1], w[2], w[3]);
           }
