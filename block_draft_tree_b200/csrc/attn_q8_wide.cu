@@ -16,12 +16,13 @@
 //     slots (K, V alternating) in the 128-byte swizzle that the MMAs read;
 //     tree rows likewise.  The codes never pass through a staging buffer, and
 //     any page size works, since no box has to fit a page;
-//   * warp 1 issues PV_A(i), QK_A(i+1), PV_B(i), QK_B(i+1): one tile's softmax
-//     overlaps the other tile's MMAs;
-//   * warpgroups 1 and 2 are the softmax of A and B, a row per thread: the 128
+//   * warp 1 issues the MMAs by steps of 64 tokens, PV_A(j), QK_A(j+2), PV_B(j),
+//     QK_B(j+2): a tile's scores have two buffers, so the softmax of step j + 1
+//     runs while the products around step j do;
+//   * warpgroups 1 and 2 are the softmax of A and B, a row per thread: the 64
 //     scores in registers, the context bound and the ancestor bitset as masks,
 //     P over the scores' columns, O rescaled only when the reference moves.
-// Registers go to where they are needed by setmaxnreg: 40 + 2 x 160 + 152.
+// Registers go to where they are needed by setmaxnreg: 40 + 2 x 136 + 200.
 // KV splits write (O, m, l) partials that attn_q8_combine merges.  Every wait
 // is bounded; one that gives up raises DDT_ERR_TIMEOUT.
 #include "attn_q8.cuh"
@@ -34,7 +35,7 @@ namespace {
 constexpr int BM = 128, BN = 128, D = 128;
 constexpr int kThreads = 512;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColO = 256;   // tile t: S at 128 t, O at 256 + 128 t
+constexpr uint32_t kColS = 0, kColO = 256;   // tile t: S of step j at 128 t + 64 (j & 1), O at 256 + 128 t
 constexpr int kHalfTile = BN * 128;          // a 64-wide slice: 128 rows x 128 bytes
 constexpr int kTile = 2 * kHalfTile;         // 32 KB
 constexpr int kSlots = 4;
@@ -43,12 +44,13 @@ constexpr float kHead = 9.f;                 // P of a new maximum is 2^9: at mo
 constexpr int kTreeTop = 4;                  // tree rows as f16: amax in [2^4, 2^5)
 constexpr int kGroup = 16;                   // tokens that share a place and an exponent
 constexpr int kGroups = BN / kGroup;
+constexpr int SN = 64;                       // tokens of a softmax step: half a KV tile
 
 struct __align__(16) Shared {
   uint64_t q_full;
   uint64_t kv_full[kSlots], kv_empty[kSlots];
   uint64_t sc_full[4];        // the scales of tile i (ring of 4 tiles)
-  uint64_t s_full[2], p_full[2];
+  uint64_t s_full[2][2], p_full[2][2];  // [tile][step & 1]
   uint64_t o_full, drain;
   long long wait_cycles;
   uint32_t tmem_base;
@@ -69,9 +71,9 @@ template <int N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-// kind::f16, f16 x f16 -> f32, M = 128, N = 128, A K-major; B K-major or MN-major.
-constexpr uint32_t idesc_f16(bool b_mn_major) {
-  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+// kind::f16, f16 x f16 -> f32, M = 128, A K-major; B K-major or MN-major.
+constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
 }
 // One lane of a converged warp.  The issuer's branch is on elect.sync and not
 // on a lane number: the compiler then keeps the operands of the MMAs in
@@ -130,10 +132,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
       mbar_init(&sh->kv_empty[s], 1);
       mbar_init(&sh->sc_full[s], 1);
     }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&sh->s_full[t], 1);
-      mbar_init(&sh->p_full[t], 128);
-    }
+    for (int t = 0; t < 2; ++t)
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sh->s_full[t][h], 1);
+        mbar_init(&sh->p_full[t][h], 128);
+      }
     mbar_init(&sh->o_full, 1);
     mbar_init(&sh->drain, 1);
     sh->wait_cycles = p.wait_cycles;
@@ -170,48 +173,58 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     if (warp == 1 && ntiles > 0 && elect_one()) {
       // ------------------------------------------------------------ MMA issuer
-      constexpr uint32_t kIdQK = idesc_f16(false), kIdPV = idesc_f16(true);
-      const int nt = has_b ? 2 : 1;
+      constexpr uint32_t kIdQK = idesc_f16(SN, false), kIdPV = idesc_f16(D, true);
+      const int nt = has_b ? 2 : 1, steps = 2 * ntiles;
       const uint32_t q_lo = desc_lo(sQ, 16), k_lo = desc_lo(sKV, 16), v_lo = desc_lo(sKV, kHalfTile);
-      auto qk = [&](int x, int i) {  // S_x = Q_x K_i^T
-        const uint32_t q = q_lo + x * (kTile >> 4), k = k_lo + ((2 * i) & 3) * (kTile >> 4);
+      // S_x(j) = Q_x K^T for step j: tokens 64 (j & 1) .. of tile j / 2
+      auto qk = [&](int x, int j) {
+        const uint32_t q = q_lo + x * (kTile >> 4);
+        const uint32_t k = k_lo + (j & 2) * (kTile >> 4) + (j & 1) * (SN * 128 >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (uint32_t)((kk >> 2) * kHalfTile + (kk & 3) * 32) >> 4;
-          mma_ss(tm + kColS + 128 * x, desc_of(q + off), desc_of(k + off), kIdQK, kk > 0 ? 1u : 0u);
+          mma_ss(tm + kColS + 128 * x + SN * (j & 1), desc_of(q + off), desc_of(k + off), kIdQK, kk > 0 ? 1u : 0u);
         }
-        mma_commit(&sh->s_full[x]);
       };
-      auto pv = [&](int x, int i) {  // O_x += P_x V_i, P_x in the first half of S_x
-        const uint32_t v = v_lo + ((2 * i + 1) & 3) * (kTile >> 4);
+      auto pv = [&](int x, int j) {  // O_x += P_x V, P_x in the first half of S_x(j)'s columns
+        const uint32_t v = v_lo + ((j & 2) + 1) * (kTile >> 4) + (j & 1) * (SN * 128 >> 4);
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts(tm + kColO + 128 * x, tm + kColS + 128 * x + kk * 8, desc_of(v + kk * (2048 >> 4)), kIdPV,
-                 (i > 0 || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < SN / 16; ++kk)
+          mma_ts(tm + kColO + 128 * x, tm + kColS + 128 * x + SN * (j & 1) + kk * 8, desc_of(v + kk * (2048 >> 4)),
+                 kIdPV, (j > 0 || kk > 0) ? 1u : 0u);
       };
       bool go = wait(&sh->q_full, 0, sh) && wait(&sh->kv_full[0], 0, sh);
       if (go) {
         fence_after();
-        for (int x = 0; x < nt; ++x) qk(x, 0);
+        for (int j = 0; j < 2; ++j)
+          for (int x = 0; x < nt; ++x) {
+            qk(x, j);
+            mma_commit(&sh->s_full[x][j]);
+          }
         mma_commit(&sh->kv_empty[0]);  // K_0
       }
-      for (int i = 0; go && i < ntiles; ++i) {
-        const int vs = (2 * i + 1) & 3, ks1 = (2 * i + 2) & 3;
-        const bool next = i + 1 < ntiles;
-        if (!wait(&sh->kv_full[vs], (uint32_t)(i >> 1) & 1u, sh)) break;
-        for (int x = 0; x < nt; ++x) {
-          if (!wait(&sh->p_full[x], (uint32_t)i & 1u, sh) ||
-              (next && x == 0 && !wait(&sh->kv_full[ks1], (uint32_t)((i + 1) >> 1) & 1u, sh))) {
-            go = false;
-            break;
-          }
+      // Tile i's slots: K at 2 i & 2, V behind it.  S_x(j + 2) follows PV_x(j),
+      // whose P shares its columns; S_x(j + 1) is there meanwhile, so the softmax
+      // of a step never waits for its own product.
+      for (int j = 0; go && j < steps; ++j) {
+        const int i = j >> 1;
+        const bool next = j + 2 < steps;
+        if ((j & 1) == 0)
+          go = wait(&sh->kv_full[(j & 2) + 1], (uint32_t)(i >> 1) & 1u, sh) &&
+               (!next || wait(&sh->kv_full[(j + 2) & 2], (uint32_t)((i + 1) >> 1) & 1u, sh));
+        for (int x = 0; go && x < nt; ++x) {
+          go = wait(&sh->p_full[x][j & 1], (uint32_t)i & 1u, sh);
+          if (!go) break;
           fence_after();
-          pv(x, i);
-          if (next) qk(x, i + 1);
+          pv(x, j);
+          if (next) qk(x, j + 2);
+          mma_commit(&sh->s_full[x][j & 1]);  // (also when there is no S: PV_x(j) is complete behind it)
         }
         if (!go) break;
-        mma_commit(&sh->kv_empty[vs]);             // V_i: every PV of step i issued
-        if (next) mma_commit(&sh->kv_empty[ks1]);  // K_{i+1}
+        if (j & 1) {
+          mma_commit(&sh->kv_empty[(j & 2) + 1]);           // V_i: every PV of tile i issued
+          if (next) mma_commit(&sh->kv_empty[(j + 2) & 2]);  // K_{i+1}
+        }
       }
       if (go) mma_commit(&sh->o_full);
       if (*(volatile int*)&sh->abort) {
@@ -222,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     }
   } else if (wg == 3) {
     // ------------------------------------------------------------ converter
-    regs_inc<152>();
+    regs_inc<200>();
     const int cw = warp & 3, ct = tid & 127;
     const int tok = ct >> 2, c4 = ct & 3;  // of 32 tokens; 16 elements of a 64-wide slice
     const uint32_t stride = (uint32_t)p.c.hkv * D;
@@ -386,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     asm volatile("bar.arrive 2, 384;" ::: "memory");
   } else {
     // ------------------------------------------------------------ softmax
-    regs_inc<160>();
+    regs_inc<136>();
     // ---- Q as f16 under a power of two per row: a row per softmax thread
     const int t = wg - 1;                            // softmax tile
     const int row = (warp & 3) * 32 + lane;
@@ -425,23 +438,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_col = lane_base + kColS + 128 * t, o_col = lane_base + kColO + 128 * t;
     const uint32_t* mrow = p.mask + ((int64_t)b * p.n_max + (row_valid ? jq : 0)) * p.W;
-    for (int i = 0; tile_live && i < ntiles; ++i) {
-      const int ti = t_lo + i;
-      const bool tree = ti >= nct;
-      const int base = (tree ? ti - nct : ti) * BN;
-      const int cnt = min(BN, (tree ? n : T) - base);
-      ok = __all_sync(0xFFFFFFFFu, wait(&sh->sc_full[i & 3], (uint32_t)(i >> 2) & 1u, sh) &&
-                                       wait(&sh->s_full[t], (uint32_t)i & 1u, sh));
+    for (int j = 0; tile_live && j < 2 * ntiles; ++j) {
+      const int i = j >> 1, half = j & 1;
+      const bool tree = t_lo + i >= nct;
+      const int base = (t_lo + i - (tree ? nct : 0)) * BN + half * SN;
+      const int cnt = min(SN, (tree ? n : T) - base);
+      ok = __all_sync(0xFFFFFFFFu, (half || wait(&sh->sc_full[i & 3], (uint32_t)(i >> 2) & 1u, sh)) &&
+                                       wait(&sh->s_full[t][half], (uint32_t)i & 1u, sh));
       if (!ok) break;
       fence_after();
-      uint32_t r[BN];
+      const float2* scale = &sh->scales[i & 3][half * (SN / kGroup)];
+      uint32_t r[SN];
 #pragma unroll
-      for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_col + 32 * c, r + 32 * c);
+      for (int c = 0; c < SN / 32; ++c) tmem_ld32(s_col + half * SN + 32 * c, r + 32 * c);
       tmem_ld_wait();
-      // t_j = s_j + V exponent, two scores at a time
+      // t = s + V exponent, two scores at a time
 #pragma unroll
-      for (int q = 0; q < kGroups; ++q) {
-        const float2 sc = sh->scales[i & 3][q];
+      for (int q = 0; q < SN / kGroup; ++q) {
+        const float2 sc = scale[q];
         const float f = mul * sc.x;
         const uint64_t f2 = pack2(f, f), e2 = pack2(sc.y, sc.y);
 #pragma unroll
@@ -452,9 +466,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
           r[q * 16 + e + 1] = __float_as_uint(c);
         }
       }
-      if (tree || cnt < BN) {
+      if (tree || cnt < SN) {
 #pragma unroll
-        for (int w = 0; w < BN / 32; ++w) {
+        for (int w = 0; w < SN / 32; ++w) {
           const int have = cnt - 32 * w;
           uint32_t bits = have >= 32 ? 0xFFFFFFFFu : (have > 0 ? (1u << have) - 1u : 0u);
           if (tree) bits = row_valid && (base >> 5) + w < p.W ? bits & __ldg(mrow + (base >> 5) + w) : 0u;
@@ -467,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
 #pragma unroll
       for (int e = 0; e < 4; ++e) m4[e] = __uint_as_float(r[e]);
 #pragma unroll
-      for (int e = 4; e < BN; e += 2)
+      for (int e = 4; e < SN; e += 2)
         m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
       const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       float alpha = 1.f;
@@ -481,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
       const uint64_t nm2 = pack2(-m, -m);
       // P = 2^(t - m) as f16 pairs over the scores, its sum weighted by 2^-(V exponent)
 #pragma unroll
-      for (int c = 0; c < BN / 32; ++c) {
+      for (int c = 0; c < SN / 32; ++c) {
         uint32_t pk[16];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -499,12 +513,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
           float a, z;
           unpack2(fadd2(s2[0], s2[1]), a, z);
           // (a group that is not there has weights 0 and must not meet 2^inf)
-          l = fmaf(a + z, ex2(fminf(-sh->scales[i & 3][2 * c + q].y, 126.f)), l);
+          l = fmaf(a + z, ex2(fminf(-scale[2 * c + q].y, 126.f)), l);
         }
-        tmem_st16(s_col + 16 * c, pk);
+        tmem_st16(s_col + half * SN + 16 * c, pk);
       }
-      // O_t holds PV_t(i-1) (complete: the commit behind s_full covers it)
-      if (i > 0 && __any_sync(0xFFFFFFFFu, move)) {
+      if (j > 0 && __any_sync(0xFFFFFFFFu, move)) {
+        // PV_t(j - 1) is complete behind the next commit on the other half's S
+        ok = __all_sync(0xFFFFFFFFu, wait(&sh->s_full[t][half ^ 1], (uint32_t)((j + 1) >> 1) & 1u, sh));
+        if (!ok) break;
+        fence_after();
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -517,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
       }
       tmem_st_wait();
       fence_before();
-      mbar_arrive(&sh->p_full[t]);
+      mbar_arrive(&sh->p_full[t][half]);
     }
     if (tile_live && ok && ntiles > 0) ok = __all_sync(0xFFFFFFFFu, wait(&sh->o_full, 0, sh));
     asm volatile("bar.sync 2, 384;" ::: "memory");  // the converter's marks in sh->odd are complete
