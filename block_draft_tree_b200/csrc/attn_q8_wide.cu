@@ -10,19 +10,19 @@
 // the tensor pipe, and beside it the 2^x of every score (MUFU) and the shared
 // memory that feeds the MMAs.  One CTA per SM takes two tiles of 128 rows
 // (A, B) of a kv head and KV tiles of 128 tokens, each converted once for both:
-//   * warpgroup 3 converts: codes come from global memory into registers (the
-//     next tile's loads are issued as the last one's registers are used up),
-//     become f16 by integer instructions, and go to a ring of four 32 KB
-//     slots (K, V alternating) in the 128-byte swizzle that the MMAs read;
-//     tree rows likewise.  The codes never pass through a staging buffer, and
-//     any page size works, since no box has to fit a page;
+//   * warpgroups 3 and 4 convert K and V: codes come from global memory into
+//     registers (the next tile's loads are issued as the last one's registers
+//     are used up), become f16 by integer instructions, and go to a ring of
+//     two 32 KB slots each in the 128-byte swizzle that the MMAs read; tree
+//     rows likewise.  The codes never pass through a staging buffer, and any
+//     page size works, since no box has to fit a page;
 //   * warp 1 issues the MMAs by steps of 64 tokens, PV_A(j), QK_A(j+2), PV_B(j),
 //     QK_B(j+2): a tile's scores have two buffers, so the softmax of step j + 1
 //     runs while the products around step j do;
 //   * warpgroups 1 and 2 are the softmax of A and B, a row per thread: the 64
 //     scores in registers, the context bound and the ancestor bitset as masks,
 //     P over the scores' columns, O rescaled only when the reference moves.
-// Registers go to where they are needed by setmaxnreg: 40 + 2 x 136 + 200.
+// Registers go to where they are needed by setmaxnreg: 40 + 2 x 136 + 2 x 80.
 // KV splits write (O, m, l) partials that attn_q8_combine merges.  Every wait
 // is bounded; one that gives up raises DDT_ERR_TIMEOUT.
 #include "attn_q8.cuh"
@@ -33,7 +33,8 @@ namespace ddt {
 namespace {
 
 constexpr int BM = 128, BN = 128, D = 128;
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
+constexpr int kRegs0 = 40, kRegsSoftmax = 136, kRegsConvert = 80;  // of a thread of each warpgroup
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // tile t: S of step j at 128 t + 64 (j & 1), O at 256 + 128 t
 constexpr int kHalfTile = BN * 128;          // a 64-wide slice: 128 rows x 128 bytes
@@ -56,7 +57,7 @@ struct __align__(16) Shared {
   uint32_t tmem_base;
   int abort;
   float2 scales[4][kGroups];  // (what a K product counts for, V exponent)
-  uint32_t amax[2][kGroups];  // largest magnitudes of a tree tile's groups, from two warps each
+  uint32_t amax[2][2][kGroups];  // K, V: largest magnitudes of a tree tile's groups, from two warps each
   uint32_t odd[32];           // tree rows with a non-finite V element
 };
 
@@ -96,14 +97,14 @@ __device__ __forceinline__ uint32_t desc_lo(const void* at, uint32_t lbo_bytes) 
 __device__ __forceinline__ uint32_t tile_at(int r, int ch) {
   return (uint32_t)((ch >> 3) * kHalfTile + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
 }
-// AND of v over the converter's 128 threads.
-__device__ __forceinline__ bool all_of_converter(bool v) {
+// AND of v over a converter warpgroup's 128 threads (named barrier `id`).
+__device__ __forceinline__ bool all_of_converter(int id, bool v) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)v)
+      : "r"((uint32_t)v), "r"(id)
       : "memory");
   return r != 0;
 }
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&sh->kv_full[s], 4);
       mbar_init(&sh->kv_empty[s], 1);
-      mbar_init(&sh->sc_full[s], 1);
+      mbar_init(&sh->sc_full[s], 2);
     }
     for (int t = 0; t < 2; ++t)
       for (int h = 0; h < 2; ++h) {
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
   const uint32_t tmem = sh->tmem_base;
 
   if (wg == 0) {
-    regs_dec<40>();
+    regs_dec<kRegs0>();
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     if (warp == 1 && ntiles > 0 && elect_one()) {
       // ------------------------------------------------------------ MMA issuer
@@ -233,9 +234,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
         mbar_wait_bounded(&sh->drain, 0u, &keep_going, kDrainCycles);
       }
     }
-  } else if (wg == 3) {
-    // ------------------------------------------------------------ converter
-    regs_inc<200>();
+  } else if (wg >= 3) {
+    // ------------------------------------------------------------ converters
+    regs_dec<kRegsConvert>();
+    const int kind = wg - 3, bar_id = 1 + 2 * kind;  // K, V
     const int cw = warp & 3, ct = tid & 127;
     const int tok = ct >> 2, c4 = ct & 3;  // of 32 tokens; 16 elements of a 64-wide slice
     const uint32_t stride = (uint32_t)p.c.hkv * D;
@@ -243,33 +245,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     // places and exponents of the 16-token groups of 4 tiles, a group a lane; a
     // group that is not there reads row 0 and weighs nothing
     struct LookUp {
-      int row, ek, ev;
-      bool there;
+      int row, e;
     };
+    constexpr int kMissing = 1 << 16;  // exponent of a group that is not there
+    const int8_t* exps = kind ? p.c.ve : p.c.ke;
     auto look_up = [&](int i) -> LookUp {  // of tiles i .. i + 3
-      LookUp u{0, 0, 0, false};
+      LookUp u{0, kMissing};
       const int64_t pos = ((int64_t)(t_lo + i) * kGroups + lane) * kGroup;
       if (i + (lane >> 3) < nctx && pos < T) {
         const Q8Place at = q8_place(p.c, b, pos);
         if (at.row < 0) {
-          if (cw == 0) raise_status(p.status, DDT_ERR_INVALID_ARG);
+          if (warp == 12) raise_status(p.status, DDT_ERR_INVALID_ARG);
         } else {
-          u.there = true;
           u.row = (int)at.row;
-          u.ek = p.c.ke[at.blk * p.c.hkv + kvh];
-          u.ev = p.c.ve[at.blk * p.c.hkv + kvh];
+          u.e = exps[at.blk * p.c.hkv + kvh];
         }
       }
       return u;
     };
-    // K and V codes of the next tile to convert: pass q holds slice q & 1 of
-    // tokens 32 (q / 2) + tok, of group 2 (q / 2) + (warp >= 2)
-    uint4 xk[8], xv[8];
-    const int64_t lane_off = (int64_t)kvh * D + (tok & 15) * (int64_t)stride + c4 * 16;
-    const uint8_t *k_lane = p.c.kc + lane_off, *v_lane = p.c.vc + lane_off;
-    auto load = [&](const LookUp& u, int i, int q, const uint8_t* base) {
+    // codes of the next tile to convert: pass q holds slice q & 1 of tokens
+    // 32 (q / 2) + tok, of group 2 (q / 2) + (cw >= 2)
+    uint4 x[8];
+    const uint8_t* lane_src =
+        (kind ? p.c.vc : p.c.kc) + (int64_t)kvh * D + (tok & 15) * (int64_t)stride + c4 * 16;
+    auto load = [&](const LookUp& u, int i, int q) {
       const int r = __shfl_sync(0xFFFFFFFFu, u.row, (i & 3) * 8 + (q >> 1) * 2 + (cw >> 1));
-      return ld_stream_v4(base + (uint64_t)(uint32_t)r * stride + (q & 1) * 64);
+      x[q] = ld_stream_v4(lane_src + (uint64_t)(uint32_t)r * stride + (q & 1) * 64);
     };
     // 16 elements as f16 to their two chunks of row r (of rows of two parities
     // a quarter warp writes, the swizzle gives eight different banks)
@@ -277,129 +278,129 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
       *(uint4*)(dst + tile_at(r, slice * 8 + 2 * c4)) = lo;
       *(uint4*)(dst + tile_at(r, slice * 8 + 2 * c4 + 1)) = hi;
     };
-    auto done = [&](int c) {  // load c is in its slot
+    auto slot_of = [&](int i) { return (2 * i + kind) & 3; };
+    auto slot_free = [&](int i) {
+      return __all_sync(0xFFFFFFFFu, wait(&sh->kv_empty[slot_of(i)], ((uint32_t)(i >> 1) & 1u) ^ 1u, sh));
+    };
+    auto done = [&](int i) {  // tile i is in its slot
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->kv_full[c & 3]);
+      if (lane == 0) mbar_arrive(&sh->kv_full[slot_of(i)]);
     };
     bool go = true;
     LookUp now = {}, then = {};
     if (nctx > 0) {
       now = look_up(0);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) xk[q] = load(now, 0, q, k_lane);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) xv[q] = load(now, 0, q, v_lane);
+      for (int q = 0; q < 8; ++q) load(now, 0, q);
     }
     for (int i = 0; go && i < nctx; ++i) {
-      {
-        const int src = (i & 3) * 8 + (lane & 7);
-        const int ek = __shfl_sync(0xFFFFFFFFu, now.ek, src), ev = __shfl_sync(0xFFFFFFFFu, now.ev, src);
-        const bool there = __shfl_sync(0xFFFFFFFFu, (int)now.there, src);
-        if (cw == 0 && lane < kGroups)
-          sh->scales[i & 3][lane] =
-              make_float2(q8_scale(ek), !there ? -INFINITY
-                                               : ev == DDT_Q8_EXP_NAN ? __int_as_float(0x7FC00000)
-                                                                      : (float)(q8_exp(ev) + kCodeShift));
+      const int e = __shfl_sync(0xFFFFFFFFu, now.e, (i & 3) * 8 + (lane & 7));
+      if (cw == 0) {
+        // what a K code * 2^-8 counts for; the V exponent of such a code
+        if (lane < kGroups) {
+          if (kind == 0)
+            sh->scales[i & 3][lane].x = e == kMissing ? 0.f : q8_scale(e);
+          else
+            sh->scales[i & 3][lane].y = e == kMissing ? -INFINITY
+                                                      : e == DDT_Q8_EXP_NAN ? __int_as_float(0x7FC00000)
+                                                                            : (float)(q8_exp(e) + kCodeShift);
+        }
         __syncwarp();
-        if (cw == 0 && lane == 0) mbar_arrive(&sh->sc_full[i & 3]);
+        if (lane == 0) mbar_arrive(&sh->sc_full[i & 3]);
       }
       if ((i & 3) == 1) then = look_up((i & ~3) + 4);
       if ((i & 3) == 3) now = then;  // from here on for tile i + 1
+      go = slot_free(i);
+      if (!go) break;
+      unsigned char* dst = sKV + slot_of(i) * kTile;
 #pragma unroll
-      for (int kind = 0; kind < 2; ++kind) {
-        const int c = 2 * i + kind;
-        go = go && __all_sync(0xFFFFFFFFu, wait(&sh->kv_empty[c & 3], ((uint32_t)(c >> 2) & 1u) ^ 1u, sh));
-        if (!go) break;
-        unsigned char* dst = sKV + (c & 3) * kTile;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint4 v = kind ? xv[q] : xk[q];
-          if (i + 1 < nctx) (kind ? xv : xk)[q] = load(now, i + 1, q, kind ? v_lane : k_lane);
-          store(dst, (q >> 1) * 32 + tok, q & 1,
-                make_uint4(codes_lo(v.x), codes_hi(v.x), codes_lo(v.y), codes_hi(v.y)),
-                make_uint4(codes_lo(v.z), codes_hi(v.z), codes_lo(v.w), codes_hi(v.w)));
-        }
-        done(c);
+      for (int q = 0; q < 8; ++q) {
+        const uint4 v = x[q];
+        if (i + 1 < nctx) load(now, i + 1, q);
+        store(dst, (q >> 1) * 32 + tok, q & 1, make_uint4(codes_lo(v.x), codes_hi(v.x), codes_lo(v.y), codes_hi(v.y)),
+              make_uint4(codes_lo(v.z), codes_hi(v.z), codes_lo(v.w), codes_hi(v.w)));
       }
+      done(i);
     }
     for (int i = nctx; i < ntiles; ++i) {
       // ---- a tile of tree rows: bf16 to f16 under a power of two per group
       const int row0 = (t_lo + i - nct) * BN;
+      const uint16_t* src = (kind ? p.vt : p.kt) + (((int64_t)b * p.n_max + row0) * p.c.hkv + kvh) * D + c4 * 16;
+      unsigned char* dst = sKV + slot_of(i) * kTile;
 #pragma unroll 1
-      for (int kind = 0; kind < 2; ++kind) {
-        const int c = 2 * i + kind;
-        go = all_of_converter(go);  // (the four warps leave together; amax may be written again)
+      for (int half = 0; half < 2; ++half) {  // 64 rows
+        go = all_of_converter(bar_id, go);  // (the four warps leave together; amax may be written again)
         if (!go) break;
-        const uint16_t* src = (kind ? p.vt : p.kt) + (((int64_t)b * p.n_max + row0) * p.c.hkv + kvh) * D + c4 * 16;
-        // the tile's rows in registers: pass q as for the codes
-        uint4 x[8][2];
+        uint4 w[4][2];  // pass q as for the codes
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int r = (q >> 1) * 32 + tok;
+        for (int q = 0; q < 4; ++q) {
+          const int r = half * 64 + (q >> 1) * 32 + tok;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            x[q][h] = make_uint4(0, 0, 0, 0);
-            if (row0 + r < n) x[q][h] = __ldg((const uint4*)(src + (int64_t)r * stride + (q & 1) * 64) + h);
+            w[q][h] = make_uint4(0, 0, 0, 0);
+            if (row0 + r < n) w[q][h] = __ldg((const uint4*)(src + (int64_t)r * stride + (q & 1) * 64) + h);
           }
         }
         // largest finite magnitudes, a group from two warps
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
           uint32_t m = 0;
           bool odd = false;
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            const uint4 v = x[2 * q + (h >> 1)][h & 1];
+            const uint4 v = w[2 * q + (h >> 1)][h & 1];
             m = max_finite_bf16(max_finite_bf16(max_finite_bf16(max_finite_bf16(m, v.x), v.y), v.z), v.w);
             odd |= max(max(max_bf16(v.x), max_bf16(v.y)), max(max_bf16(v.z), max_bf16(v.w))) >= 0x7F80u;
           }
-          if (odd && kind) atomicOr(&sh->odd[(row0 + q * 32 + tok) >> 5], 1u << ((row0 + q * 32 + tok) & 31));
+          const int tr = row0 + half * 64 + q * 32 + tok;
+          if (odd && kind) atomicOr(&sh->odd[tr >> 5], 1u << (tr & 31));
           m = __reduce_max_sync(0xFFFFFFFFu, m);
-          if (lane == 0) sh->amax[cw & 1][2 * q + (cw >> 1)] = m;
+          if (lane == 0) sh->amax[kind][cw & 1][half * 4 + 2 * q + (cw >> 1)] = m;
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        const uint32_t m = max(sh->amax[0][lane & 7], sh->amax[1][lane & 7]);
+        asm volatile("bar.sync %0, 128;" ::"r"(bar_id) : "memory");
+        const int gl = half * 4 + (lane & 3);
+        const uint32_t m = max(sh->amax[kind][0][gl], sh->amax[kind][1][gl]);
         const int e = min(max(f16_exponent(m, kTreeTop), DDT_Q8_EXP_MIN), DDT_Q8_EXP_MAX);
-        if (cw == 0 && lane < kGroups) {
-          if (kind == 0)
-            sh->scales[i & 3][lane].x = pow2i(e);
-          else
-            sh->scales[i & 3][lane].y = (float)e;
+        if (cw == 0) {
+          if (lane < 4) {
+            if (kind == 0)
+              sh->scales[i & 3][gl].x = pow2i(e);
+            else
+              sh->scales[i & 3][gl].y = (float)e;
+          }
+          __syncwarp();
+          if (half && lane == 0) mbar_arrive(&sh->sc_full[i & 3]);
         }
-        __syncwarp();
-        if (kind && cw == 0 && lane == 0) mbar_arrive(&sh->sc_full[i & 3]);
-        go = __all_sync(0xFFFFFFFFu, wait(&sh->kv_empty[c & 3], ((uint32_t)(c >> 2) & 1u) ^ 1u, sh));
+        if (half == 0) go = slot_free(i);
         if (!go) continue;
-        unsigned char* dst = sKV + (c & 3) * kTile;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int r = (q >> 1) * 32 + tok;
+        for (int q = 0; q < 4; ++q) {
           const float inv = pow2i(-__shfl_sync(0xFFFFFFFFu, e, (q >> 1) * 2 + (cw >> 1)));
           uint4 f[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t w[4] = {x[q][h].x, x[q][h].y, x[q][h].z, x[q][h].w};
+            uint32_t u[4] = {w[q][h].x, w[q][h].y, w[q][h].z, w[q][h].w};
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               if (kind) {  // non-finite V elements go to their rows at the end, and to no others
-                if ((w[z] & 0x7F80u) == 0x7F80u) w[z] &= 0xFFFF0000u;
-                if ((w[z] & 0x7F800000u) == 0x7F800000u) w[z] &= 0x0000FFFFu;
+                if ((u[z] & 0x7F80u) == 0x7F80u) u[z] &= 0xFFFF0000u;
+                if ((u[z] & 0x7F800000u) == 0x7F800000u) u[z] &= 0x0000FFFFu;
               }
-              w[z] = bf16x2_to_f16x2(w[z], inv);
+              u[z] = bf16x2_to_f16x2(u[z], inv);
             }
-            f[h] = make_uint4(w[0], w[1], w[2], w[3]);
+            f[h] = make_uint4(u[0], u[1], u[2], u[3]);
           }
-          store(dst, r, q & 1, f[0], f[1]);
+          store(dst, half * 64 + (q >> 1) * 32 + tok, q & 1, f[0], f[1]);
         }
-        done(c);
+        if (half) done(i);
       }
       if (!go) break;
     }
-    asm volatile("bar.arrive 2, 384;" ::: "memory");
+    asm volatile("bar.arrive 2, 512;" ::: "memory");
   } else {
     // ------------------------------------------------------------ softmax
-    regs_inc<136>();
+    regs_inc<kRegsSoftmax>();
     // ---- Q as f16 under a power of two per row: a row per softmax thread
     const int t = wg - 1;                            // softmax tile
     const int row = (warp & 3) * 32 + lane;
@@ -537,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
       mbar_arrive(&sh->p_full[t][half]);
     }
     if (tile_live && ok && ntiles > 0) ok = __all_sync(0xFFFFFFFFu, wait(&sh->o_full, 0, sh));
-    asm volatile("bar.sync 2, 384;" ::: "memory");  // the converter's marks in sh->odd are complete
+    asm volatile("bar.sync 2, 512;" ::: "memory");  // the converter's marks in sh->odd are complete
     fence_after();
 
     // ---- epilogue: O rows to the output or to a split's partial
@@ -613,6 +614,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
 }  // namespace
 
 cudaError_t launch_attn_q8_wide(const AttnQ8Params& p, int pairs, cudaStream_t stream) {
+  // the warpgroups' shares have to come out of what the block is launched with
+  static_assert(kRegs0 + 2 * kRegsSoftmax + 2 * kRegsConvert <= 96 * kThreads / 128, "register split");
+  static const int regs = [] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, attn_q8_wide_kernel) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (regs < 96) return cudaErrorInvalidConfiguration;
   const size_t smem = 1024 + (size_t)(2 + kSlots) * kTile + sizeof(Shared);
   const cudaError_t e = ensure_smem_attr((const void*)attn_q8_wide_kernel, smem);
   if (e != cudaSuccess) return e;
