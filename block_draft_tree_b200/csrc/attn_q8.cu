@@ -123,8 +123,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int tile = blockIdx.x, split = blockIdx.y, grp = blockIdx.z;
-  const int b = grp / p.c.hkv, kvh = grp % p.c.hkv;
+  const int tile = blockIdx.x, split = blockIdx.y;
   const int R = p.n_max * p.g;
   const int q0 = tile * RT;
   uint64_t* full = bars + warp * kStages;
@@ -135,6 +134,8 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
   }
   __syncwarp();
   pdl_wait();
+  const int grp = blockIdx.z;
+  const int b = grp / p.c.hkv, kvh = grp % p.c.hkv;
   int n, T;
   attn_q8_lengths(p, b, tile == 0 && split == 0 && kvh == 0 && tid == 0, n, T);
   const int nhalf = (T + kHalf - 1) / kHalf;     // 16-token pieces of the context
@@ -585,19 +586,22 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
   }
 }
 
-// Merge the splits' partials: a CTA per query row, its warps take the splits in
-// turn (many splits of few rows is what long contexts give), then join.
+// Merge the splits' partials.  WPR = 1: a warp per query row (many rows of few
+// splits: large trees).  WPR = 4: the CTA's warps take one row's splits in turn
+// and join (few rows of many splits: long contexts).
 constexpr int kCombineWarps = 4;
-template <int D>
+template <int D, int WPR>
 __global__ void __launch_bounds__(32 * kCombineWarps) attn_q8_combine(const AttnQ8Params p) {
   constexpr int E = D / 32;  // elements a lane
   __shared__ float s_o[kCombineWarps][D];
   __shared__ float2 s_ml[kCombineWarps];
-  const int R = p.n_max * p.g;
-  const int qr = blockIdx.x, grp = blockIdx.y, b = grp / p.c.hkv, kvh = grp % p.c.hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int R = p.n_max * p.g;
+  const int qr = blockIdx.x * (kCombineWarps / WPR) + (WPR == 1 ? warp : 0);
+  const int grp = blockIdx.y, b = grp / p.c.hkv, kvh = grp % p.c.hkv;
   pdl_wait();
   pdl_trigger();
+  if (WPR == 1 && qr >= R) return;
   int n, T;
   attn_q8_lengths(p, b, false, n, T);
   const bool live = qr < n * p.g;
@@ -605,13 +609,13 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_q8_combine(const Attn
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   const int64_t row = (int64_t)grp * p.nsplit * R + qr;
-  constexpr int kFly = 8;
-  for (int s0 = warp; live && s0 < p.nsplit; s0 += kFly * kCombineWarps) {
+  constexpr int kFly = WPR == 1 ? 4 : 8;
+  for (int s0 = WPR == 1 ? 0 : warp; live && s0 < p.nsplit; s0 += kFly * WPR) {
     float2 ml[kFly];
     float v[kFly][E];
 #pragma unroll
     for (int f = 0; f < kFly; ++f) {
-      const int s = s0 + f * kCombineWarps;
+      const int s = s0 + f * WPR;
       ml[f] = make_float2(-INFINITY, 0.f);
       if (s < p.nsplit) {
         const int64_t at = row + (int64_t)s * R;
@@ -648,30 +652,43 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_q8_combine(const Attn
       }
     M = to;
   }
+  if (WPR > 1) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
-  if (lane == 0) s_ml[warp] = make_float2(M, L);
-  __syncthreads();
-  const int d0 = threadIdx.x * 2;
-  if (d0 >= D) return;
-  M = -INFINITY;
-  L = 0.f;
+    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
+    if (lane == 0) s_ml[warp] = make_float2(M, L);
+    __syncthreads();
+    if (warp != 0) return;
+    M = -INFINITY;
+    L = 0.f;
 #pragma unroll
-  for (int w = 0; w < kCombineWarps; ++w) M = fmaxf(M, s_ml[w].x);
-  float x = 0.f, y = 0.f;
+    for (int w = 0; w < kCombineWarps; ++w) M = fmaxf(M, s_ml[w].x);
 #pragma unroll
-  for (int w = 0; w < kCombineWarps; ++w)
-    if (s_ml[w].x != -INFINITY) {
-      const float a = ex2(s_ml[w].x - M);
-      L = fmaf(s_ml[w].y, a, L);
-      x = fmaf(s_o[w][d0], a, x);
-      y = fmaf(s_o[w][d0 + 1], a, y);
-    }
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kCombineWarps; ++w)
+      if (s_ml[w].x != -INFINITY) {
+        const float a = ex2(s_ml[w].x - M);
+        L = fmaf(s_ml[w].y, a, L);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(s_o[w][lane * E + e], a, acc[e]);
+      }
+  }
   const float inv = M == -INFINITY ? 0.f : 1.f / L;
   const int64_t at = row_index(p, b, kvh, qr);
-  *(uint32_t*)(p.out + at * D + d0) = f32x2_to_bf16x2(x * inv, y * inv);
-  if (p.lse_out && d0 == 0)
+  uint32_t* dst = (uint32_t*)(p.out + at * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = f32x2_to_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (p.lse_out && lane == 0)
     p.lse_out[at] = M == -INFINITY ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+}
+
+template <int D>
+cudaError_t launch_combine(const AttnQ8Params& p, cudaStream_t stream) {
+  const unsigned groups = (unsigned)(p.batch * p.c.hkv), R = (unsigned)(p.n_max * p.g);
+  const dim3 block(32 * kCombineWarps);
+  if (p.nsplit > 8) return launch_pdl(attn_q8_combine<D, 4>, dim3(R, groups), block, 0, stream, 0, p);
+  return launch_pdl(attn_q8_combine<D, 1>, dim3((R + kCombineWarps - 1) / kCombineWarps, groups), block, 0,
+                    stream, 0, p);
 }
 
 struct Plan {
@@ -680,19 +697,19 @@ struct Plan {
 };
 
 // The wide kernel's pairs of row tiles and KV splits (steps: tiles of 128
-// tokens): the fewest waves x tiles, a split's partials and their merge
-// counted as kMergeTiles tiles.
+// tokens): the fewest waves x tiles of a CTA, a split's partials and their
+// merge counted as kMergeTiles tiles (measured on 16 ragged trees of 129 rows:
+// 380 us in three splits, 348 us in one).
 Plan plan_wide(const ddt_attn_q8_args* a, long R) {
-  constexpr long kMergeTiles = 3;
-  Plan pl;
-  pl.nr = 0;
+  constexpr long kMergeTiles = 8;
+  Plan pl = {};
   pl.tiles = (int)((R + 255) / 256);
   const long base = (long)pl.tiles * a->batch * a->cache.hkv, sms = device_sm_count();
   const long tiles = (a->max_ctx + 127) / 128 + (a->n_max + 127) / 128;
   long best = -1;
-  for (long s = 1; s <= 32 && s <= tiles; ++s) {
+  for (long s = 1; s <= 64 && s <= tiles; ++s) {
     const long ts = (tiles + s - 1) / s, sp = (tiles + ts - 1) / ts;
-    const long cost = (base * sp + sms - 1) / sms * ts + (sp > 1 ? kMergeTiles : 0);
+    const long cost = (base * sp + sms - 1) / sms * (ts + (sp > 1 ? kMergeTiles : 0));
     if (best < 0 || cost < best) {
       best = cost;
       pl.steps_per_split = (int)ts;
@@ -702,11 +719,12 @@ Plan plan_wide(const ddt_attn_q8_args* a, long R) {
   return pl;
 }
 
-// Row tiles of 8, 16, 24 or 32 rows and KV splits.
+// d = 128 with more than kWideRows rows per kv head takes the wide kernel,
+// anything else row tiles of 8, 16, 24 or 32 rows and KV splits of this file's.
 Plan plan_of(const ddt_attn_q8_args* a) {
-  Plan pl;
   const long R = (long)a->n_max * (a->hq / a->cache.hkv);
   if (a->cache.d == 128 && R > kWideRows) return plan_wide(a, R);
+  Plan pl;
   pl.nr = (int)std::min(4L, (R + 7) / 8);
   pl.tiles = (int)((R + 8 * pl.nr - 1) / (8 * pl.nr));
   const long base = (long)pl.tiles * a->batch * a->cache.hkv;
@@ -714,9 +732,9 @@ Plan plan_of(const ddt_attn_q8_args* a) {
   const long slots = (long)device_sm_count() * (pl.nr <= 2 ? 3 : 2);
   // as many splits as fill the device, of at least 2 steps a warp; long
   // contexts in splits of at most kLong steps, so that ragged ones even out
+  constexpr long kLong = 64;
   long ns = std::max(1L, slots / std::max(1L, base));
   ns = std::min(ns, std::max(1L, steps / (2 * kWarps)));
-  constexpr long kLong = 64;
   ns = std::max(ns, steps / kLong);
   ns = std::min(ns, 65535L);
   pl.steps_per_split = (int)((steps + ns - 1) / ns);
@@ -774,7 +792,6 @@ size_t attn_q8_workspace_size(const ddt_attn_q8_args* a) {
 
 ddt_status launch_attn_q8(const ddt_attn_q8_args* a, void* ws, cudaStream_t stream) {
   if (a->batch == 0) return DDT_OK;
-  const Plan pl = plan_of(a);
   AttnQ8Params p;
   p.c = q8_view(&a->cache);
   p.q = (const uint16_t*)a->q;
@@ -793,12 +810,13 @@ ddt_status launch_attn_q8(const ddt_attn_q8_args* a, void* ws, cudaStream_t stre
   p.out = (uint16_t*)a->out;
   p.lse_out = a->lse_out;
   p.status = a->dev_status;
+  p.wait_cycles = wait_limit_cycles();
+  const Plan pl = plan_of(a);
   p.nsplit = pl.nsplit;
   p.steps_per_split = pl.steps_per_split;
   const size_t rows = (size_t)a->batch * a->cache.hkv * pl.nsplit * a->n_max * p.g;
   p.part_o = pl.nsplit > 1 ? (float*)ws : nullptr;
   p.part_ml = pl.nsplit > 1 ? (float2*)((char*)ws + align256(rows * a->cache.d * sizeof(float))) : nullptr;
-  p.wait_cycles = wait_limit_cycles();
   cudaError_t e;
   if (pl.nr == 0) {
     p.box_rows = 0;
@@ -814,9 +832,7 @@ ddt_status launch_attn_q8(const ddt_attn_q8_args* a, void* ws, cudaStream_t stre
   }
   if (e != cudaSuccess) return DDT_ERR_CUDA;
   if (pl.nsplit > 1) {
-    const dim3 grid(a->n_max * p.g, a->batch * a->cache.hkv), block(32 * kCombineWarps);
-    e = a->cache.d == 128 ? launch_pdl(attn_q8_combine<128>, grid, block, 0, stream, 0, p)
-                          : launch_pdl(attn_q8_combine<64>, grid, block, 0, stream, 0, p);
+    e = a->cache.d == 128 ? launch_combine<128>(p, stream) : launch_combine<64>(p, stream);
     if (e != cudaSuccess) return DDT_ERR_CUDA;
   }
   return DDT_OK;

@@ -33,6 +33,27 @@ __device__ __forceinline__ void attn_q8_lengths(const AttnQ8Params& p, int b, bo
   }
 }
 
+// The (sequence, kv head) group of a block's z index: longest contexts first,
+// so that the last blocks to start are short ones (measured on 16 trees of 129
+// rows over 1024 .. 16384 tokens: 570 us in order, 348 us so).  Batches beyond
+// kOrdered run in order.
+constexpr int kOrdered = 256;
+__device__ __forceinline__ int group_of(const AttnQ8Params& p, int z, int* s_pick) {
+  if (p.batch == 1 || p.batch > kOrdered) return z;
+  const int want = z / p.c.hkv;
+  for (int t = threadIdx.x; t < p.batch; t += blockDim.x) {
+    const int mine = p.ctx_len[t];
+    int before = 0;
+    for (int j = 0; j < p.batch; ++j) {
+      const int other = __ldg(p.ctx_len + j);
+      before += other > mine || (other == mine && j < t);
+    }
+    if (before == want) *s_pick = t;
+  }
+  __syncthreads();
+  return *s_pick * p.c.hkv + z % p.c.hkv;
+}
+
 Q8View q8_view(const ddt_q8_cache* c);
 
 }  // namespace ddt

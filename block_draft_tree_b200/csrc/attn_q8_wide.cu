@@ -22,9 +22,11 @@
 //   * warpgroups 1 and 2 are the softmax of A and B, a row per thread: the 64
 //     scores in registers, the context bound and the ancestor bitset as masks,
 //     P over the scores' columns, O rescaled only when the reference moves.
-// Registers go to where they are needed by setmaxnreg: 40 + 2 x 136 + 2 x 80.
+// Registers go to where they are needed by setmaxnreg: 40 + 2 x 120 + 2 x 96.
 // KV splits write (O, m, l) partials that attn_q8_combine merges.  Every wait
 // is bounded; one that gives up raises DDT_ERR_TIMEOUT.
+#include <cfloat>
+
 #include "attn_q8.cuh"
 #include "launch.h"
 #include "tcgen05.cuh"
@@ -34,7 +36,7 @@ namespace {
 
 constexpr int BM = 128, BN = 128, D = 128;
 constexpr int kThreads = 640;
-constexpr int kRegs0 = 40, kRegsSoftmax = 136, kRegsConvert = 80;  // of a thread of each warpgroup
+constexpr int kRegs0 = 40, kRegsSoftmax = 120, kRegsConvert = 96;  // of a thread of each warpgroup
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // tile t: S of step j at 128 t + 64 (j & 1), O at 256 + 128 t
 constexpr int kHalfTile = BN * 128;          // a 64-wide slice: 128 rows x 128 bytes
@@ -55,7 +57,7 @@ struct __align__(16) Shared {
   uint64_t o_full, drain;
   long long wait_cycles;
   uint32_t tmem_base;
-  int abort;
+  int abort, pick;
   float2 scales[4][kGroups];  // (what a K product counts for, V exponent)
   uint32_t amax[2][2][kGroups];  // K, V: largest magnitudes of a tree tile's groups, from two warps each
   uint32_t odd[32];           // tree rows with a non-finite V element
@@ -124,8 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
   Shared* sh = (Shared*)(sKV + kSlots * kTile);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
-  const int pair = blockIdx.x, split = blockIdx.y, grp = blockIdx.z;
-  const int b = grp / p.c.hkv, kvh = grp % p.c.hkv;
+  const int pair = blockIdx.x, split = blockIdx.y;
   if (tid == 0) {
     mbar_init(&sh->q_full, 8);
     for (int s = 0; s < kSlots; ++s) {
@@ -153,11 +154,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_wait();
+  const int grp = group_of(p, blockIdx.z, &sh->pick);
+  const int b = grp / p.c.hkv, kvh = grp % p.c.hkv;
   const int g = p.g, R = p.n_max * g, q0 = pair * 2 * BM;
   int n, T;
   attn_q8_lengths(p, b, pair == 0 && split == 0 && kvh == 0 && tid == 0, n, T);
   // a tile works when one of its rows belongs to a tree row
-  const bool has_a = q0 < n * g, has_b = q0 + BM < n * g;
+  const int live = n * g;
+  const bool has_a = q0 < live, has_b = q0 + BM < live;
   const int nct = (T + BN - 1) / BN;
   const int ntt = (n + BN - 1) / BN;
   const int t_lo = min(split * p.steps_per_split, nct + ntt);
@@ -236,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     }
   } else if (wg >= 3) {
     // ------------------------------------------------------------ converters
-    regs_dec<kRegsConvert>();
+    static_assert(kRegsConvert == 96, "what the block is launched with");
     const int kind = wg - 3, bar_id = 1 + 2 * kind;  // K, V
     const int cw = warp & 3, ct = tid & 127;
     const int tok = ct >> 2, c4 = ct & 3;  // of 32 tokens; 16 elements of a 64-wide slice
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
         // what a K code * 2^-8 counts for; the V exponent of such a code
         if (lane < kGroups) {
           if (kind == 0)
-            sh->scales[i & 3][lane].x = e == kMissing ? 0.f : q8_scale(e);
+            sh->scales[i & 3][lane].x = e == kMissing ? 1.f : q8_scale(e);
           else
             sh->scales[i & 3][lane].y = e == kMissing ? -INFINITY
                                                       : e == DDT_Q8_EXP_NAN ? __int_as_float(0x7FC00000)
@@ -406,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     const int row = (warp & 3) * 32 + lane;
     const int qr = q0 + t * BM + row, jq = qr / g;
     const bool tile_live = t == 0 ? has_a : has_b;
-    const bool row_valid = tile_live && qr < n * g;
+    const bool row_valid = tile_live && qr < live;
     const int64_t out_row = ((int64_t)b * p.n_max + jq) * p.hq + kvh * g + qr % g;
     float mul = 0.f;
     if (tile_live && ntiles > 0) {
@@ -453,20 +457,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
 #pragma unroll
       for (int c = 0; c < SN / 32; ++c) tmem_ld32(s_col + half * SN + 32 * c, r + 32 * c);
       tmem_ld_wait();
-      // t = s + V exponent, two scores at a time
-#pragma unroll
-      for (int q = 0; q < SN / kGroup; ++q) {
-        const float2 sc = scale[q];
-        const float f = mul * sc.x;
-        const uint64_t f2 = pack2(f, f), e2 = pack2(sc.y, sc.y);
-#pragma unroll
-        for (int e = 0; e < kGroup; e += 2) {
-          float a, c;
-          unpack2(ffma2(pack2(__uint_as_float(r[q * 16 + e]), __uint_as_float(r[q * 16 + e + 1])), f2, e2), a, c);
-          r[q * 16 + e] = __float_as_uint(a);
-          r[q * 16 + e + 1] = __float_as_uint(c);
-        }
-      }
       if (tree || cnt < SN) {
 #pragma unroll
         for (int w = 0; w < SN / 32; ++w) {
@@ -478,13 +468,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
             if (!((bits >> e) & 1u)) r[32 * w + e] = 0xFF800000u;  // -inf
         }
       }
-      float m4[4];
+      // t = f s + V exponent; its largest from the largest s of each group (f > 0)
+      float f[SN / kGroup], ev[SN / kGroup], top = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) m4[e] = __uint_as_float(r[e]);
+      for (int q = 0; q < SN / kGroup; ++q) {
+        const float2 sc = scale[q];
+        f[q] = mul * sc.x;
+        if (f[q] < FLT_MIN) f[q] = FLT_MIN;  // (all that it multiplies is nothing then; -inf has to stay -inf)
+        ev[q] = sc.y;
+        float m2[2] = {__uint_as_float(r[q * 16]), __uint_as_float(r[q * 16 + 1])};
 #pragma unroll
-      for (int e = 4; e < SN; e += 2)
-        m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
-      const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        for (int e = 2; e < kGroup; e += 2)
+          m2[(e >> 1) & 1] = fmax3(m2[(e >> 1) & 1], __uint_as_float(r[q * 16 + e]), __uint_as_float(r[q * 16 + e + 1]));
+        top = fmaxf(top, fmaf(fmaxf(m2[0], m2[1]), f[q], ev[q]));
+      }
       float alpha = 1.f;
       const bool move = top > m_ref + (kSlack + kHead);
       if (move) {
@@ -493,19 +490,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
         l *= alpha;
       }
       const float m = m_ref == -INFINITY ? 0.f : m_ref;
-      const uint64_t nm2 = pack2(-m, -m);
-      // P = 2^(t - m) as f16 pairs over the scores, its sum weighted by 2^-(V exponent)
+      // P = 2^(t - m) as f16 pairs over the scores, its sum weighted by 2^-(V
+      // exponent).  (A quarter of the 2^x on the FMA pipe instead of MUFU gave
+      // 1 %, more of them lost: the issue slots are as scarce.)
 #pragma unroll
       for (int c = 0; c < SN / 32; ++c) {
         uint32_t pk[16];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
+          const int gq = 2 * c + q;
+          const uint64_t f2 = pack2(f[gq], f[gq]), c2 = pack2(ev[gq] - m, ev[gq] - m);
           uint64_t s2[2] = {0ull, 0ull};
 #pragma unroll
           for (int e = 0; e < kGroup; e += 2) {
-            const int at = 32 * c + 16 * q + e;
+            const int at = 16 * gq + e;
+            const uint64_t x2 = ffma2(pack2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), f2, c2);
             float a, z;
-            unpack2(fadd2(pack2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), nm2), a, z);
+            unpack2(x2, a, z);
             a = ex2(a);
             z = ex2(z);
             s2[(e >> 1) & 1] = fadd2(s2[(e >> 1) & 1], pack2(a, z));
@@ -513,8 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
           }
           float a, z;
           unpack2(fadd2(s2[0], s2[1]), a, z);
-          // (a group that is not there has weights 0 and must not meet 2^inf)
-          l = fmaf(a + z, ex2(fminf(-scale[2 * c + q].y, 126.f)), l);
+          l = fmaf(a + z, ev[gq] == -INFINITY ? 0.f : ex2(-ev[gq]), l);  // (a group that is not there: nothing)
         }
         tmem_st16(s_col + half * SN + 16 * c, pk);
       }
@@ -542,6 +542,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     fence_after();
 
     // ---- epilogue: O rows to the output or to a split's partial
+    if (l != l)
+      m_ref = 0.f;  // a row of NaN scores alone has no reference: any number carries its NaN on
+    else if (m_ref == -INFINITY)
+      l = 0.f;      // a row that saw nothing
     const bool final_out = p.nsplit == 1;
     const bool has = ok && row_valid && ntiles > 0 && l != 0.f;  // (NaN counts as a sum)
     const float inv = has ? 1.f / l : 0.f;
@@ -593,8 +597,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
                                __uint_as_float(o[4 * e + 3]));
       }
     }
-    // (a row of NaN scores alone has no reference: any number carries its NaN on)
-    if (l != l) m_ref = 0.f;
     if (writes && final_out) {
       if (p.lse_out) p.lse_out[out_row] = has ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
     } else if (writes) {
