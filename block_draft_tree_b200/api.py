@@ -717,7 +717,9 @@ def lm_head_walk(hidden: torch.Tensor, weight: torch.Tensor, tok: torch.Tensor,
 # element's value is code * 2^exponent.
 
 Q8_BLOCKS = (16, 32, 64, 128)
-Q8_EXP_MIN, Q8_EXP_MAX = -48, 48
+Q8_EXP_MIN, Q8_EXP_MAX, Q8_EXP_NAN = -48, 48, -128
+
+_F8, _I8, _BF16, _I32 = torch.float8_e4m3fn, torch.int8, torch.bfloat16, torch.int32
 
 
 def _q8_cache(fn: str, b: int, k_cache, v_cache, k_exp, v_exp, block: int, page_table) -> Q8Cache:
@@ -727,54 +729,92 @@ def _q8_cache(fn: str, b: int, k_cache, v_cache, k_exp, v_exp, block: int, page_
     exponents [pages, page_size / block, hkv]."""
     if block not in Q8_BLOCKS:
         raise DDTError("%s: block must be one of %s, got %r" % (fn, Q8_BLOCKS, block))
-    if k_cache.dim() != 4 or k_cache.dtype != torch.float8_e4m3fn or not k_cache.is_contiguous():
+    shape = k_cache.shape
+    if len(shape) != 4 or k_cache.dtype is not _F8 or not k_cache.is_contiguous():
         raise DDTError("%s: caches must be contiguous float8_e4m3fn [.., .., hkv, d], got %s %s"
-                       % (fn, k_cache.dtype, tuple(k_cache.shape)))
-    if v_cache.shape != k_cache.shape:
+                       % (fn, k_cache.dtype, tuple(shape)))
+    if v_cache.shape != shape:
         raise DDTError("%s: the V cache must have the K cache's shape" % fn)
-    _check_types(fn, (v_cache, torch.float8_e4m3fn), (k_exp, torch.int8), (v_exp, torch.int8),
-                 (page_table, torch.int32))
-    n0, n1, hkv, d = k_cache.shape
-    if page_table is None and n0 != b:
-        raise DDTError("%s: a dense cache must have %d sequences, got %d" % (fn, b, n0))
-    if page_table is not None:
-        if page_table.dim() != 2 or page_table.shape[0] != b:
-            raise DDTError("%s: page_table must be [%d, max_pages]" % (fn, b))
-        if n1 % block:
-            raise DDTError("%s: pages of %d tokens do not hold whole blocks of %d" % (fn, n1, block))
+    for t, dt in ((v_cache, _F8), (k_exp, _I8), (v_exp, _I8)):
+        if t.dtype is not dt or not t.is_contiguous():
+            raise DDTError("%s: expected contiguous %s tensors, got %s" % (fn, dt, t.dtype))
+    n0, n1, hkv, d = shape
     want = (n0, -(-n1 // block), hkv)
-    if tuple(k_exp.shape) != want or tuple(v_exp.shape) != want:
+    if k_exp.shape != want or v_exp.shape != want:
         raise DDTError("%s: exponents must be %s, got %s and %s"
                        % (fn, want, tuple(k_exp.shape), tuple(v_exp.shape)))
-    c = Q8Cache()
-    c.k_cache, c.v_cache = k_cache.data_ptr() or None, v_cache.data_ptr() or None
-    c.k_exp, c.v_exp = k_exp.data_ptr() or None, v_exp.data_ptr() or None
-    c.block, c.hkv, c.d = block, hkv, d
+    ptrs = (k_cache.data_ptr() or None, v_cache.data_ptr() or None, k_exp.data_ptr() or None,
+            v_exp.data_ptr() or None)
     if page_table is None:
-        c.page_table, c.page_size, c.max_pages, c.num_pages, c.t_max = None, 0, 0, 0, n1
-    else:
-        c.page_table, c.page_size, c.max_pages = page_table.data_ptr(), n1, page_table.shape[1]
-        c.num_pages, c.t_max = n0, 0
-    return c
+        if n0 != b:
+            raise DDTError("%s: a dense cache must have %d sequences, got %d" % (fn, b, n0))
+        return Q8Cache(*ptrs, None, block, 0, 0, 0, n1, hkv, d)
+    if page_table.dtype is not _I32 or not page_table.is_contiguous():
+        raise DDTError("%s: expected contiguous torch.int32 tensors, got %s"
+                       % (fn, page_table.dtype))
+    pages = page_table.shape
+    if len(pages) != 2 or pages[0] != b:
+        raise DDTError("%s: page_table must be [%d, max_pages]" % (fn, b))
+    if n1 % block:
+        raise DDTError("%s: pages of %d tokens do not hold whole blocks of %d" % (fn, n1, block))
+    return Q8Cache(*ptrs, page_table.data_ptr(), block, n1, pages[1], n0, 0, hkv, d)
 
 
 def _check_rows_q8(fn: str, k, v, k_cache):
-    """Raise unless k and v are contiguous bf16 [batch, n, hkv, d] rows for the cache."""
-    if k.dim() != 4 or k_cache.dim() != 4 or k.shape[2:] != k_cache.shape[2:]:
+    """Raise unless k and v are contiguous bf16 [batch, n, hkv, d] rows for the
+    cache.  Returns k's shape."""
+    shape, cache = k.shape, k_cache.shape
+    if len(shape) != 4 or len(cache) != 4 or shape[2:] != cache[2:]:
         raise DDTError("%s: rows must be [batch, n, %s], got %s"
-                       % (fn, ", ".join(str(x) for x in k_cache.shape[2:]), tuple(k.shape)))
-    if v.shape != k.shape:
+                       % (fn, ", ".join(str(x) for x in cache[2:]), tuple(shape)))
+    if v.shape != shape:
         raise DDTError("%s: the V rows must have the K rows' shape" % fn)
-    _check_types(fn, (k, torch.bfloat16), (v, torch.bfloat16))
+    for t in (k, v):
+        if t.dtype is not _BF16 or not t.is_contiguous():
+            raise DDTError("%s: expected contiguous %s tensors, got %s" % (fn, _BF16, t.dtype))
+    return shape
 
 
-def _check_vectors(fn: str, b: int, **named):
-    """Raise unless every given tensor is a contiguous int32 [b]."""
-    for name, t in named.items():
-        if t is not None and (tuple(t.shape) != (b,) or t.dtype != torch.int32
-                              or not t.is_contiguous()):
-            raise DDTError("%s: %s must be a contiguous int32 [%d], got %s %s"
-                           % (fn, name, b, t.dtype, tuple(t.shape)))
+def _vector(fn: str, name: str, b: int, t):
+    """The address of an optional contiguous int32 [b]; raises for any other tensor."""
+    if t is None:
+        return None
+    if t.shape != (b,) or t.dtype is not _I32 or not t.is_contiguous():
+        raise DDTError("%s: %s must be a contiguous int32 [%d], got %s %s"
+                       % (fn, name, b, t.dtype, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _status_q8(fn: str, t):
+    """The address of an optional status word."""
+    if t is None:
+        return None
+    if t.dtype is not _I32 or not t.is_contiguous() or t.numel() < 1:
+        raise DDTError("%s: dev_status must be a contiguous int32 tensor" % fn)
+    return t.data_ptr()
+
+
+def _call_q8(name: str, args, dev: int):
+    """The entry point ``name`` on device ``dev`` (made current) and its current stream."""
+    f = getattr(load_library(), name)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch.cuda.current_device() == dev:
+        rc = f(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, stream)
+    if rc:
+        _check(rc, name)
+
+
+def _device_q8(*ts) -> int:
+    """The index of the one CUDA device that every given tensor (None skipped) is on."""
+    dev = ts[0].get_device()
+    for t in ts:
+        if t is not None and (t.get_device() != dev or dev < 0):
+            _need_cuda(*ts)
+            raise DDTError("all tensors must be on one device")
+    return dev
 
 
 def kv_append_q8(k_new: torch.Tensor, v_new: torch.Tensor, ctx_len: torch.Tensor,
@@ -788,25 +828,16 @@ def kv_append_q8(k_new: torch.Tensor, v_new: torch.Tensor, ctx_len: torch.Tensor
     ``k_cache`` / ``v_cache`` float8_e4m3fn, dense [batch, t_max, hkv, d] or a
     pool [pages, page_size, hkv, d] with ``page_table`` [batch, max_pages];
     ``k_exp`` / ``v_exp`` int8 [.., ceil(tokens / block), hkv]."""
-    lib = load_library()
     fn = "kv_append_q8"
-    _check_rows_q8(fn, k_new, v_new, k_cache)
-    b, n_max = k_new.shape[:2]
-    _check_vectors(fn, b, ctx_len=ctx_len, n_new=n_new)
-    _check_types(fn, (dev_status, torch.int32))
-    a = KVAppendQ8Args()
-    a.cache = _q8_cache(fn, b, k_cache, v_cache, k_exp, v_exp, block, page_table)
-    dev = _need_cuda(k_new, v_new, ctx_len, k_cache, v_cache, k_exp, v_exp, n_new, page_table,
+    b, n_max, _, _ = _check_rows_q8(fn, k_new, v_new, k_cache)
+    ctx = _vector(fn, "ctx_len", b, ctx_len)
+    a = KVAppendQ8Args(_q8_cache(fn, b, k_cache, v_cache, k_exp, v_exp, block, page_table),
+                       k_new.data_ptr() or None, v_new.data_ptr() or None,
+                       _vector(fn, "n_new", b, n_new), ctx, ctx if advance else None, b, n_max,
+                       _status_q8(fn, dev_status))
+    dev = _device_q8(k_new, v_new, ctx_len, k_cache, v_cache, k_exp, v_exp, n_new, page_table,
                      dev_status)
-    a.k_new, a.v_new = k_new.data_ptr() or None, v_new.data_ptr() or None
-    a.n_new = None if n_new is None else n_new.data_ptr()
-    a.ctx_len = ctx_len.data_ptr()
-    a.ctx_len_out = ctx_len.data_ptr() if advance else None
-    a.batch, a.n_max = b, n_max
-    a.dev_status = None if dev_status is None else dev_status.data_ptr()
-    with torch.cuda.device(dev):
-        rc = lib.ddt_kv_append_q8(ctypes.byref(a), _stream(dev))
-    _check(rc, "ddt_kv_append_q8")
+    _call_q8("ddt_kv_append_q8", (ctypes.byref(a),), dev)
 
 
 def kv_commit_q8(k_tree: torch.Tensor, v_tree: torch.Tensor, acc_len: torch.Tensor,
@@ -818,27 +849,22 @@ def kv_commit_q8(k_tree: torch.Tensor, v_tree: torch.Tensor, acc_len: torch.Tens
     at :func:`kv_append_q8`): the root's and the accepted rows of the tree K/V
     are quantised behind the context, and (``advance``) ``ctx_len`` grows in
     place by acc_len + 1."""
-    lib = load_library()
     fn = "kv_commit_q8"
-    _check_rows_q8(fn, k_tree, v_tree, k_cache)
-    b, n_max = k_tree.shape[:2]
-    _check_vectors(fn, b, acc_len=acc_len, ctx_len=ctx_len)
-    if acc_nodes.dim() != 2 or acc_nodes.shape[0] != b:
+    b, n_max, _, _ = _check_rows_q8(fn, k_tree, v_tree, k_cache)
+    nodes = acc_nodes.shape
+    if len(nodes) != 2 or nodes[0] != b:
         raise DDTError("%s: acc_nodes must be [%d, L]" % (fn, b))
-    _check_types(fn, (acc_nodes, torch.int32), (dev_status, torch.int32))
-    a = KVCommitQ8Args()
-    a.cache = _q8_cache(fn, b, k_cache, v_cache, k_exp, v_exp, block, page_table)
-    dev = _need_cuda(k_tree, v_tree, acc_len, acc_nodes, ctx_len, k_cache, v_cache, k_exp, v_exp,
+    if acc_nodes.dtype is not _I32 or not acc_nodes.is_contiguous():
+        raise DDTError("%s: expected contiguous torch.int32 tensors, got %s"
+                       % (fn, acc_nodes.dtype))
+    ctx = _vector(fn, "ctx_len", b, ctx_len)
+    a = KVCommitQ8Args(_q8_cache(fn, b, k_cache, v_cache, k_exp, v_exp, block, page_table),
+                       k_tree.data_ptr(), v_tree.data_ptr(), _vector(fn, "acc_len", b, acc_len),
+                       acc_nodes.data_ptr() or None, ctx, ctx if advance else None, b, n_max,
+                       nodes[1], _status_q8(fn, dev_status))
+    dev = _device_q8(k_tree, v_tree, acc_len, acc_nodes, ctx_len, k_cache, v_cache, k_exp, v_exp,
                      page_table, dev_status)
-    a.k_tree, a.v_tree = k_tree.data_ptr(), v_tree.data_ptr()
-    a.acc_len, a.acc_nodes = acc_len.data_ptr(), acc_nodes.data_ptr() or None
-    a.ctx_len = ctx_len.data_ptr()
-    a.ctx_len_out = ctx_len.data_ptr() if advance else None
-    a.batch, a.n_max, a.L = b, n_max, acc_nodes.shape[1]
-    a.dev_status = None if dev_status is None else dev_status.data_ptr()
-    with torch.cuda.device(dev):
-        rc = lib.ddt_kv_commit_q8(ctypes.byref(a), _stream(dev))
-    _check(rc, "ddt_kv_commit_q8")
+    _call_q8("ddt_kv_commit_q8", (ctypes.byref(a),), dev)
 
 
 def kv_read_q8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_exp: torch.Tensor,
@@ -848,55 +874,45 @@ def kv_read_q8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_exp: torch.Tensor
     """``ddt_kv_read_q8``: positions first[b] + r (first None: 0), r < n_max, of
     the 8-bit cache (described at :func:`kv_append_q8`) as bf16.  Returns (k, v)
     [batch, n_max, hkv, d]; rows at or past ctx_len[b] are 0."""
-    lib = load_library()
     fn = "kv_read_q8"
     b = ctx_len.shape[0] if ctx_len.dim() == 1 else -1
-    _check_vectors(fn, b, ctx_len=ctx_len, first=first)
-    _check_types(fn, (dev_status, torch.int32))
+    ctx = _vector(fn, "ctx_len", b, ctx_len)
     if n_max < 0:
         raise DDTError("%s: n_max must not be negative" % fn)
-    a = KVReadQ8Args()
-    a.cache = _q8_cache(fn, b, k_cache, v_cache, k_exp, v_exp, block, page_table)
-    dev = _need_cuda(k_cache, v_cache, k_exp, v_exp, ctx_len, first, page_table, dev_status)
-    hkv, d = k_cache.shape[2:]
-    k = torch.empty((b, n_max, hkv, d), dtype=torch.bfloat16, device=dev)
-    v = torch.empty_like(k)
-    a.ctx_len, a.first = ctx_len.data_ptr(), None if first is None else first.data_ptr()
-    a.k_out, a.v_out = k.data_ptr() or None, v.data_ptr() or None
-    a.batch, a.n_max = b, n_max
-    a.dev_status = None if dev_status is None else dev_status.data_ptr()
-    with torch.cuda.device(dev):
-        rc = lib.ddt_kv_read_q8(ctypes.byref(a), _stream(dev))
-    _check(rc, "ddt_kv_read_q8")
+    c = _q8_cache(fn, b, k_cache, v_cache, k_exp, v_exp, block, page_table)
+    start = _vector(fn, "first", b, first)
+    dev = _device_q8(k_cache, v_cache, k_exp, v_exp, ctx_len, first, page_table, dev_status)
+    kv = torch.empty((2, b, n_max, c.hkv, c.d), dtype=_BF16, device=k_cache.device)
+    k, v = kv.unbind(0)
+    a = KVReadQ8Args(c, ctx, start, k.data_ptr() or None, v.data_ptr() or None, b, n_max,
+                     _status_q8(fn, dev_status))
+    _call_q8("ddt_kv_read_q8", (ctypes.byref(a),), dev)
     return k, v
 
 
 def _attn_q8_args(q, k_cache, v_cache, k_exp, v_exp, k_tree, v_tree, mask, n_nodes, ctx_len,
                   max_ctx, block, scale, page_table, out, lse_out, dev_status) -> AttnQ8Args:
     fn = "tree_attn_q8"
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         raise DDTError("%s: q must be [batch, n_max, hq, d]" % fn)
-    b, n_max, hq, d = q.shape
-    _check_rows_q8(fn, k_tree, v_tree, k_cache)
-    if tuple(k_tree.shape[:2]) != (b, n_max) or k_tree.shape[3] != d:
+    b, n_max, hq, d = shape
+    tree = _check_rows_q8(fn, k_tree, v_tree, k_cache)
+    if tree[0] != b or tree[1] != n_max or tree[3] != d:
         raise DDTError("%s: tree K must be [%d, %d, hkv, %d], got %s"
-                       % (fn, b, n_max, d, tuple(k_tree.shape)))
-    if tuple(mask.shape) != (b, n_max, mask_words(n_max)):
+                       % (fn, b, n_max, d, tuple(tree)))
+    if mask.shape != (b, n_max, mask_words(n_max)):
         raise DDTError("%s: mask must be [%d, %d, %d], got %s"
                        % (fn, b, n_max, mask_words(n_max), tuple(mask.shape)))
-    _check_types(fn, (q, torch.bfloat16), (mask, torch.int32), (dev_status, torch.int32))
-    _check_vectors(fn, b, n_nodes=n_nodes, ctx_len=ctx_len)
-    a = AttnQ8Args()
-    a.cache = _q8_cache(fn, b, k_cache, v_cache, k_exp, v_exp, block, page_table)
-    a.q, a.ctx_len, a.max_ctx = q.data_ptr(), ctx_len.data_ptr(), int(max_ctx)
-    a.k_tree, a.v_tree = k_tree.data_ptr(), v_tree.data_ptr()
-    a.mask, a.n_nodes = mask.data_ptr(), n_nodes.data_ptr()
-    a.batch, a.n_max, a.hq = b, n_max, hq
-    a.scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    a.out = out.data_ptr()
-    a.lse_out = None if lse_out is None else lse_out.data_ptr()
-    a.dev_status = None if dev_status is None else dev_status.data_ptr()
-    return a
+    for t, dt in ((q, _BF16), (mask, _I32)):
+        if t.dtype is not dt or not t.is_contiguous():
+            raise DDTError("%s: expected contiguous %s tensors, got %s" % (fn, dt, t.dtype))
+    return AttnQ8Args(_q8_cache(fn, b, k_cache, v_cache, k_exp, v_exp, block, page_table),
+                      q.data_ptr(), _vector(fn, "ctx_len", b, ctx_len), int(max_ctx),
+                      k_tree.data_ptr(), v_tree.data_ptr(), mask.data_ptr(),
+                      _vector(fn, "n_nodes", b, n_nodes), b, n_max, hq,
+                      1.0 / math.sqrt(d) if scale is None else float(scale), out.data_ptr(),
+                      None if lse_out is None else lse_out.data_ptr(), _status_q8(fn, dev_status))
 
 
 def tree_attn_q8_workspace_size(q, k_cache, v_cache, k_exp, v_exp, k_tree, v_tree, mask, n_nodes,
@@ -918,18 +934,23 @@ def tree_attn_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     at :func:`kv_append_q8`); the tree rows' own K/V stay bf16.  An ordinary
     decoding step is n_max = 1 with mask word 1.  Returns out bf16 [batch,
     n_max, hq, d] (and lse f32 [batch, n_max, hq] when asked)."""
-    lib = load_library()
     a = _attn_q8_args(q, k_cache, v_cache, k_exp, v_exp, k_tree, v_tree, mask, n_nodes, ctx_len,
                       max_ctx, block, scale, page_table, q, None, dev_status)
-    dev = _need_cuda(q, k_cache, v_cache, k_exp, v_exp, k_tree, v_tree, mask, n_nodes, ctx_len,
+    dev = _device_q8(q, k_cache, v_cache, k_exp, v_exp, k_tree, v_tree, mask, n_nodes, ctx_len,
                      page_table, dev_status)
     out = torch.empty_like(q)
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if want_lse else None
-    a.out, a.lse_out = out.data_ptr(), None if lse is None else lse.data_ptr()
-    with torch.cuda.device(dev):
-        nb = int(lib.ddt_tree_attn_q8_workspace_size(ctypes.byref(a)))
-        # scratch of this call alone: calls on other streams and captured graphs have their own
-        ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
-        rc = lib.ddt_tree_attn_q8(ctypes.byref(a), _ptr(ws), nb, _stream(dev))
-    _check(rc, "ddt_tree_attn_q8")
+    a.out = out.data_ptr()
+    lse = None
+    if want_lse:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        a.lse_out = lse.data_ptr()
+    ref = ctypes.byref(a)
+    if torch.cuda.current_device() == dev:
+        nb = load_library().ddt_tree_attn_q8_workspace_size(ref)
+    else:
+        with torch.cuda.device(dev):
+            nb = load_library().ddt_tree_attn_q8_workspace_size(ref)
+    # scratch of this call alone: calls on other streams and captured graphs have their own
+    ws = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
+    _call_q8("ddt_tree_attn_q8", (ref, ws.data_ptr() if nb else None, nb), dev)
     return (out, lse) if want_lse else out
