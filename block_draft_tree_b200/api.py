@@ -882,8 +882,9 @@ def kv_read_q8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_exp: torch.Tensor
     c = _q8_cache(fn, b, k_cache, v_cache, k_exp, v_exp, block, page_table)
     start = _vector(fn, "first", b, first)
     dev = _device_q8(k_cache, v_cache, k_exp, v_exp, ctx_len, first, page_table, dev_status)
-    kv = torch.empty((2, b, n_max, c.hkv, c.d), dtype=_BF16, device=k_cache.device)
-    k, v = kv.unbind(0)
+    shape = (b, n_max, c.hkv, c.d)
+    k = torch.empty(shape, dtype=_BF16, device=k_cache.device)
+    v = torch.empty(shape, dtype=_BF16, device=k_cache.device)
     a = KVReadQ8Args(c, ctx, start, k.data_ptr() or None, v.data_ptr() or None, b, n_max,
                      _status_q8(fn, dev_status))
     _call_q8("ddt_kv_read_q8", (ctypes.byref(a),), dev)

@@ -70,22 +70,10 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(WriteParams p) {
   const int h = unit % hkv, kv = (unit / hkv) & 1;
   const int64_t pos0 = ((ctx >> p.c.block_log2) + unit / (2 * hkv)) << p.c.block_log2;
   bool on = unit < p.units && ctx >= 0 && pos0 < ctx + n;
-  Q8Place at{-1, -1};
-  if (on) {
-    at = q8_place(p.c, b, pos0);
-    if (at.row < 0) {
-      if (tu == 0) raise_status(p.status, DDT_ERR_INVALID_ARG);
-      on = false;
-    }
-  }
+  // the rows are asked for before the place that they go to is looked up
   const int64_t limit = p.c.page_table ? ctx + n : p.c.t_max;
   const int64_t end = min(ctx + n, limit);
-  if (on && end < ctx + n && pos0 + BLOCK > end && tu == 0)
-    raise_status(p.status, DDT_ERR_INVALID_ARG);  // a dense block cut off by t_max
-  uint8_t* codes = (kv ? p.c.vc : p.c.kc) + (at.row * hkv + h) * D + (tu % CH) * 8;
-  int8_t* exps = (kv ? p.c.ve : p.c.ke) + at.blk * hkv + h;
   const uint4* src = (kv ? p.v_new : p.k_new) + ((int64_t)b * p.n_max * hkv + h) * CH + tu % CH;
-
   uint4 x[NP];
   uint32_t fresh = 0, older = 0;  // bit i: pass i holds a new row / an older code
   uint32_t amax = 0;  // the largest magnitude's bits
@@ -100,12 +88,25 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(WriteParams p) {
       if (p.acc_len && r > 0) r = p.acc_nodes[(int64_t)b * p.L + r - 1];
       if (r >= 0 && r < p.n_max) {
         fresh |= 1u << i;
-        x[i] = __ldg(src + r * hkv * CH);
+        x[i] = ld_stream_v4(src + r * hkv * CH);
       } else if (tu % CH == 0) {
         raise_status(p.status, DDT_ERR_INVALID_ARG);
       }
     }
   }
+  Q8Place at{-1, -1};
+  if (on) {
+    at = q8_place(p.c, b, pos0);
+    if (at.row < 0) {
+      if (tu == 0) raise_status(p.status, DDT_ERR_INVALID_ARG);
+      on = false;
+      fresh = 0;
+    }
+  }
+  if (on && end < ctx + n && pos0 + BLOCK > end && tu == 0)
+    raise_status(p.status, DDT_ERR_INVALID_ARG);  // a dense block cut off by t_max
+  uint8_t* codes = (kv ? p.c.vc : p.c.kc) + (at.row * hkv + h) * D + (tu % CH) * 8;
+  int8_t* exps = (kv ? p.c.ve : p.c.ke) + at.blk * hkv + h;
   const bool had = on && pos0 < ctx;
   const int e_was = had ? *exps : DDT_Q8_EXP_MIN;
   const int e_old = q8_exp(e_was);
@@ -176,32 +177,31 @@ struct ReadParams {
   Q8View c;
   const int32_t *ctx_len, *first;
   uint4 *k_out, *v_out;
-  int n_max;
+  int n_max, rows;            // output rows of a sequence, of a CTA
   int32_t* status;
 };
 
-constexpr int kReadRows = 16;  // output rows of a CTA
+constexpr int kReadRows = 32;  // output rows of a CTA, at most
 
-// One 16-byte vector of codes (16 elements) -> two of bf16; s: 2^(e + 8).
-__device__ __forceinline__ void decode16(uint4 c, float s, uint4& lo, uint4& hi) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  uint32_t o[8];
+// 8 codes -> 8 bf16; s: 2^(e + 8).
+__device__ __forceinline__ uint4 decode8(uint2 c, float s) {
+  const uint32_t w[2] = {c.x, c.y};
+  uint32_t o[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < 2; ++q) {
     const float2 a = f16x2_to_f32x2(codes_lo(w[q])), z = f16x2_to_f32x2(codes_hi(w[q]));
     o[2 * q] = f32x2_to_bf16x2(a.x * s, a.y * s);
     o[2 * q + 1] = f32x2_to_bf16x2(z.x * s, z.y * s);
   }
-  lo = make_uint4(o[0], o[1], o[2], o[3]);
-  hi = make_uint4(o[4], o[5], o[6], o[7]);
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 __global__ void __launch_bounds__(kThreads) read_q8_kernel(ReadParams p) {
   __shared__ Q8Place s_at[kReadRows];
   const int tid = threadIdx.x, b = blockIdx.y, kv = blockIdx.z;
-  const int r0 = blockIdx.x * kReadRows;
+  const int r0 = blockIdx.x * p.rows;
   pdl_wait();
-  if (tid < kReadRows) {
+  if (tid < p.rows) {
     Q8Place at{-1, -1};
     const int64_t first = p.first ? p.first[b] : 0;
     const int64_t pos = first + r0 + tid;
@@ -216,27 +216,27 @@ __global__ void __launch_bounds__(kThreads) read_q8_kernel(ReadParams p) {
   }
   __syncthreads();
   pdl_trigger();
-  const int vecs = p.c.hkv * p.c.d / 16;  // 16-code vectors of a row
-  const int per_head = p.c.d / 16;
-  const uint4* codes = (const uint4*)(kv ? p.c.vc : p.c.kc);
+  const int vecs = p.c.hkv * p.c.d / 8;  // 8-code vectors of a row: a warp writes 512 bytes in a row
+  const int per_head = p.c.d / 8;
+  const uint2* codes = (const uint2*)(kv ? p.c.vc : p.c.kc);
   const int8_t* exps = kv ? p.c.ve : p.c.ke;
-  uint4* out = kv ? p.v_out : p.k_out;
-  const int rows = min(kReadRows, p.n_max - r0);
+  const int rows = min(p.rows, p.n_max - r0);
   const int items = rows * vecs;
-  constexpr int kFly = 4;  // vectors in flight per thread
+  uint4* out = (kv ? p.v_out : p.k_out) + ((int64_t)b * p.n_max + r0) * vecs;
+  constexpr int kFly = 8;  // vectors in flight per thread
   for (int i0 = tid; i0 < items; i0 += kThreads * kFly) {
-    uint4 v[kFly];
+    uint2 v[kFly];
     int e[kFly];
 #pragma unroll
     for (int q = 0; q < kFly; ++q) {
       const int i = i0 + q * kThreads;
-      v[q] = make_uint4(0, 0, 0, 0);
+      v[q] = make_uint2(0, 0);
       e[q] = 0;
       if (i < items) {
-        const int r = i / vecs, x = i % vecs;
+        const int r = i / vecs, x = i - r * vecs;
         const Q8Place at = s_at[r];
         if (at.row >= 0) {
-          v[q] = ld_stream_v4(codes + at.row * vecs + x);
+          v[q] = __ldcs(codes + at.row * vecs + x);
           e[q] = __ldg(exps + at.blk * p.c.hkv + x / per_head);
         }
       }
@@ -244,12 +244,7 @@ __global__ void __launch_bounds__(kThreads) read_q8_kernel(ReadParams p) {
 #pragma unroll
     for (int q = 0; q < kFly; ++q) {
       const int i = i0 + q * kThreads;
-      if (i >= items) break;
-      uint4 lo, hi;
-      decode16(v[q], q8_scale(e[q]), lo, hi);
-      uint4* dst = out + (((int64_t)b * p.n_max + r0) * vecs + i) * 2;
-      dst[0] = lo;
-      dst[1] = hi;
+      if (i < items) __stcs(out + i, decode8(v[q], q8_scale(e[q])));
     }
   }
 }
@@ -348,7 +343,11 @@ ddt_status launch_kv_read_q8(const ddt_kv_read_q8_args* a, cudaStream_t stream) 
   p.v_out = (uint4*)a->v_out;
   p.n_max = a->n_max;
   p.status = a->dev_status;
-  const dim3 grid((a->n_max + kReadRows - 1) / kReadRows, a->batch, 2);
+  // 32 rows a CTA where that still gives every SM several (8 contexts of up to
+  // 32768 tokens: 244 us, 254 us with 16), 8 where the call is small
+  const int64_t ctas = (int64_t)((a->n_max + kReadRows - 1) / kReadRows) * a->batch * 2;
+  p.rows = ctas >= 8 * device_sm_count() ? kReadRows : kReadRows / 4;
+  const dim3 grid((a->n_max + p.rows - 1) / p.rows, a->batch, 2);
   return launch_pdl(read_q8_kernel, grid, dim3(kThreads), 0, stream, 0, p) == cudaSuccess ? DDT_OK
                                                                                           : DDT_ERR_CUDA;
 }
