@@ -587,9 +587,9 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
 }
 
 // Merge the splits' partials.  WPR = 1: a warp per query row (many rows of few
-// splits: large trees).  WPR = 4: the CTA's warps take one row's splits in turn
+// splits: large trees).  WPR = 8: the CTA's warps take one row's splits in turn
 // and join (few rows of many splits: long contexts).
-constexpr int kCombineWarps = 4;
+constexpr int kCombineWarps = 8;
 template <int D, int WPR>
 __global__ void __launch_bounds__(32 * kCombineWarps) attn_q8_combine(const AttnQ8Params p) {
   constexpr int E = D / 32;  // elements a lane
@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) attn_q8_combine(const Attn
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   const int64_t row = (int64_t)grp * p.nsplit * R + qr;
-  constexpr int kFly = WPR == 1 ? 4 : 8;
+  constexpr int kFly = 4;
   for (int s0 = WPR == 1 ? 0 : warp; live && s0 < p.nsplit; s0 += kFly * WPR) {
     float2 ml[kFly];
     float v[kFly][E];
@@ -686,7 +686,7 @@ template <int D>
 cudaError_t launch_combine(const AttnQ8Params& p, cudaStream_t stream) {
   const unsigned groups = (unsigned)(p.batch * p.c.hkv), R = (unsigned)(p.n_max * p.g);
   const dim3 block(32 * kCombineWarps);
-  if (p.nsplit > 8) return launch_pdl(attn_q8_combine<D, 4>, dim3(R, groups), block, 0, stream, 0, p);
+  if (p.nsplit > 8) return launch_pdl(attn_q8_combine<D, kCombineWarps>, dim3(R, groups), block, 0, stream, 0, p);
   return launch_pdl(attn_q8_combine<D, 1>, dim3((R + kCombineWarps - 1) / kCombineWarps, groups), block, 0,
                     stream, 0, p);
 }

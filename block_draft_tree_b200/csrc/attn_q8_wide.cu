@@ -78,10 +78,8 @@ __device__ __forceinline__ void regs_dec() {
 constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
 }
-// One lane of a converged warp.  The issuer's branch is on elect.sync and not
-// on a lane number: the compiler then keeps the operands of the MMAs in
-// uniform registers (measured: 65 cycles an MMA of 128 x 128 x 16, which is
-// the tensor pipe's rate, against 108 to 156 under `lane == 0`).
+// One lane of a converged warp (the MMA issuer's: 661 us for 8 trees of 257 rows
+// over 8192 tokens, 681 us under `lane == 0`, at the step that took it).
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
@@ -137,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     for (int t = 0; t < 2; ++t)
       for (int h = 0; h < 2; ++h) {
         mbar_init(&sh->s_full[t][h], 1);
-        mbar_init(&sh->p_full[t][h], 128);
+        mbar_init(&sh->p_full[t][h], 4);
       }
     mbar_init(&sh->o_full, 1);
     mbar_init(&sh->drain, 1);
@@ -405,34 +403,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
   } else {
     // ------------------------------------------------------------ softmax
     regs_inc<kRegsSoftmax>();
-    // ---- Q as f16 under a power of two per row: a row per softmax thread
     const int t = wg - 1;                            // softmax tile
     const int row = (warp & 3) * 32 + lane;
     const int qr = q0 + t * BM + row, jq = qr / g;
     const bool tile_live = t == 0 ? has_a : has_b;
     const bool row_valid = tile_live && qr < live;
-    const int64_t out_row = ((int64_t)b * p.n_max + jq) * p.hq + kvh * g + qr % g;
+    const int qr0 = q0 + t * BM + (warp & 3) * 32;   // the warp's first row
+    auto out_row = [&](int q) { return ((int64_t)b * p.n_max + q / g) * p.hq + kvh * g + q % g; };
+    // ---- Q as f16 under a power of two per row: half a warp loads a row
     float mul = 0.f;
     if (tile_live && ntiles > 0) {
-      const uint4* src = (const uint4*)(p.q + out_row * D);
-      uint32_t m = 0;
-      if (row_valid) {
-  #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint4 v = __ldg(src + i);
-          m = max_finite_bf16(max_finite_bf16(max_finite_bf16(max_finite_bf16(m, v.x), v.y), v.z), v.w);
-        }
-      }
-      const int e = m ? max(f16_exponent(m, 14), -126) : 0;
-      const float inv = pow2i(-e);
-      mul = p.scale_log2 * pow2i(e);
       unsigned char* dst = sQ + t * kTile;
-  #pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row_valid) v = __ldg(src + i);
-        *(uint4*)(dst + tile_at(row, i)) = make_uint4(bf16x2_to_f16x2(v.x, inv), bf16x2_to_f16x2(v.y, inv),
-                                                      bf16x2_to_f16x2(v.z, inv), bf16x2_to_f16x2(v.w, inv));
+#pragma unroll
+      for (int r0 = 0; r0 < 32; r0 += 16) {
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + 2 * i + (lane >> 4);
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (qr0 + r < live) v[i] = __ldg((const uint4*)(p.q + out_row(qr0 + r) * D) + (lane & 15));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + 2 * i + (lane >> 4);
+          uint32_t m = max_finite_bf16(max_finite_bf16(max_finite_bf16(max_finite_bf16(0, v[i].x), v[i].y), v[i].z), v[i].w);
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          const int e = m ? max(f16_exponent(m, 14), -126) : 0;
+          const float inv = pow2i(-e);
+          *(uint4*)(dst + tile_at((warp & 3) * 32 + r, lane & 15)) =
+              make_uint4(bf16x2_to_f16x2(v[i].x, inv), bf16x2_to_f16x2(v[i].y, inv), bf16x2_to_f16x2(v[i].z, inv),
+                         bf16x2_to_f16x2(v[i].w, inv));
+          const float f = __shfl_sync(0xFFFFFFFFu, p.scale_log2 * pow2i(e), (lane & 1) * 16);
+          if ((lane >> 1) == (r0 >> 1) + i) mul = f;  // lanes 2 i, 2 i + 1 own these two rows
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -535,7 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
       }
       tmem_st_wait();
       fence_before();
-      mbar_arrive(&sh->p_full[t][half]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->p_full[t][half]);
     }
     if (tile_live && ok && ntiles > 0) ok = __all_sync(0xFFFFFFFFu, wait(&sh->o_full, 0, sh));
     asm volatile("bar.sync 2, 512;" ::: "memory");  // the converter's marks in sh->odd are complete
@@ -550,7 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     const bool has = ok && row_valid && ntiles > 0 && l != 0.f;  // (NaN counts as a sum)
     const float inv = has ? 1.f / l : 0.f;
     const bool writes = final_out ? qr < R : row_valid;
-    const int64_t prow = ((int64_t)grp * p.nsplit + split) * R + qr;
+    const int64_t part0 = ((int64_t)grp * p.nsplit + split) * R;
+    unsigned char* stage = smem + (t * 4 + (warp & 3)) * (32 * D * 4);
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
@@ -580,27 +586,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
           }
         }
       }
-      if (!writes) {
-      } else if (final_out) {
-        uint32_t pk[16];
+      if (final_out) {
+        if (writes) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          pk[e] = f32x2_to_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-        uint4* dst = (uint4*)(p.out + out_row * D + 32 * c);
+          for (int e = 0; e < 16; ++e)
+            pk[e] = f32x2_to_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          uint4* dst = (uint4*)(p.out + out_row(qr) * D + 32 * c);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dst[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+          for (int e = 0; e < 4; ++e) dst[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+        }
       } else {
-        float4* dst = (float4*)(p.part_o + prow * D + 32 * c);
+        // through shared memory (every product has read it), so that a warp writes whole rows
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
-                               __uint_as_float(o[4 * e + 3]));
+          *(uint4*)(stage + lane * 512 + (((8 * c + e) ^ lane) << 4)) =
+              make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
       }
     }
+    const uint32_t write_rows = __ballot_sync(0xFFFFFFFFu, writes && !final_out);
+    if (write_rows) {
+      float* dst = p.part_o + (part0 + qr0) * D + 4 * lane;
+#pragma unroll 8
+      for (int r = 0; r < 32; ++r)
+        if ((write_rows >> r) & 1u) *(float4*)(dst + r * D) = *(const float4*)(stage + r * 512 + ((lane ^ r) << 4));
+    }
     if (writes && final_out) {
-      if (p.lse_out) p.lse_out[out_row] = has ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+      if (p.lse_out) p.lse_out[out_row(qr)] = has ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
     } else if (writes) {
-      p.part_ml[prow] = has ? make_float2(m_ref, l) : make_float2(-INFINITY, 0.f);
+      p.part_ml[part0 + qr] = has ? make_float2(m_ref, l) : make_float2(-INFINITY, 0.f);
     }
   }
   pdl_trigger();
