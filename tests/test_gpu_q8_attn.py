@@ -298,3 +298,62 @@ def test_two_streams_and_two_graphs_at_once():
     torch.cuda.synchronize()
     for i in range(2):
         assert torch.equal(outs[i], want[i]) and torch.equal(eager[i], want[i])
+
+
+@pytest.mark.parametrize("n,hq,hkv,d", [(3, 8, 1, 128), (3, 8, 1, 64), (1, 17, 1, 128), (33, 1, 1, 128), (8, 4, 1, 64)])
+def test_row_tiles(n, hq, hkv, d):
+    """Three tiles of 8 rows, and the last row beyond a tile."""
+    Case(n, hq, hkv, d, ctx=(100, 31), seed=n + hq).go()
+
+
+@pytest.mark.parametrize("n,hq", [(1, 8), (70, 1)])
+@pytest.mark.parametrize("page", [0, 16, 48])
+def test_small_and_odd_caches(n, hq, page):
+    """Caches shorter than a tile's box, lengths that are no multiple of the
+    block, pages that are no power of two and no multiple of a step."""
+    for tokens in (1, 5, 17, 100):
+        Case(n, hq, 1, 128, page=page, ctx=(tokens, tokens // 2), seed=tokens, tokens=tokens).go()
+
+
+@pytest.mark.parametrize("n,hq,batch", [(1, 2, 300), (40, 1, 300), (40, 1, 37)])
+def test_many_ragged_sequences(n, hq, batch):
+    """More sequences than are sorted by length, and fewer; equal lengths among them."""
+    Case(n, hq, 1, 128, page=64, ctx=[(i * 37) % 201 for i in range(batch)], seed=batch).go()
+
+
+def test_no_cache_at_all():
+    """max_ctx 0: the tree alone, whatever the cache's size."""
+    for n in (4, 70):
+        c = Case(n, 4, 2, 128, ctx=(0, 0), seed=n)
+        c.max_ctx = 0
+        c.go()
+        empty = torch.empty((2, 0, 2, 128), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+        exps = torch.empty((2, 0, 2), dtype=torch.int8, device=DEV)
+        out = api.tree_attn_q8(c.q, empty, empty, exps, exps, c.kt, c.vt, _pack(c.see), _i32(c.n_nodes), _i32(c.ctx), 0)
+        assert torch.equal(out, c.run()[0])
+
+
+def test_repeated_calls_agree_to_the_bit():
+    """No result depends on the order in which blocks run."""
+    for n in (1, 40, 140):
+        c = Case(n, 8, 2, 128, page=64, ctx=(3000, 50, 1111), seed=n)
+        first = c.run()
+        for _ in range(5):
+            again = c.run()
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("n,page", [(1, 0), (1, 48), (70, 0), (140, 64)])
+def test_waits_that_run_out_are_reported(n, page):
+    """With a bound of a few cycles the kernels' waits give up: the status says
+    so, and the next call with the default bound is right.  (The kernel for few
+    rows waits for copies that may have landed when it first looks.)"""
+    c = Case(n, 8, 1, 128, page=page, ctx=(2000, 900), seed=n)
+    api.set_wait_limit(4)
+    try:
+        c.run()
+        torch.cuda.synchronize()
+        assert int(c.status) == 5 or (n == 1 and int(c.status) == 0)
+    finally:
+        api.set_wait_limit(0)
+    c.go()
