@@ -26,8 +26,8 @@
 // nothing.  A lane reads its own fragments: for K, lane (g, c) holds tokens g,
 // g + 8 and two 16-byte chunks, with the d index permuted alike in Q's
 // fragments; for V, lane (g, c) holds tokens 2c, 2c+1, 8+2c, 9+2c and chunk g,
-// whose pairs one byte permute interleaves while it spreads them for the
-// conversion to f16; P^T turns between the products by movmatrix.
+// whose pairs one byte permute interleaves for the conversion to f16;
+// P^T turns between the products by movmatrix.
 #include <algorithm>
 #include <type_traits>
 
@@ -53,7 +53,7 @@ constexpr int kStep = 2 * kHalf;       // tokens of a step
 constexpr float kSlack = 4.f;          // the reference moves when a score passes it by 2^4
 constexpr float kHead = 11.f;          // P of a new maximum is 2^11
 constexpr long kWideRows = 32;         // rows per kv head beyond which d = 128 takes the wide kernel
-constexpr int kTreeTop = 4;            // tree rows as f16: amax in [2^4, 2^5)
+constexpr int kTreeTop = 8;            // tree rows as f16: amax in [2^8, 2^9), as large as codes
 
 // D += A (16x16, row) * B (16x8, col), f16 inputs, f32 accumulators.
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -173,12 +173,12 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
     }
     return u;
   };
-  // What a K code * 2^-8 counts for, and the V exponent of such a code: NaN for
+  // What a K code counts for, and the V exponent: NaN for
   // a block of NaN, -inf for a half that is not there (its weights are then 0).
   auto k_scale = [](const LookUp& u) { return q8_scale(u.ek); };
   auto v_exp = [](const LookUp& u) {
     return u.row < 0 ? -INFINITY
-                     : u.ev == DDT_Q8_EXP_NAN ? __int_as_float(0x7FC00000) : (float)(q8_exp(u.ev) + kCodeShift);
+                     : u.ev == DDT_Q8_EXP_NAN ? __int_as_float(0x7FC00000) : (float)q8_exp(u.ev);
   };
   unsigned char* my = ring + warp * kStages * S::kStageBytes;
   // Issue iteration `it` (its look-up in `row`) into its stage.
@@ -362,14 +362,17 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
         }
       }
     }
-    // (codes past the context are finite whatever they are, and weigh 0)
     const int have = T - (first + it * kWarps) * kStep;
-    const uint32_t bits = have >= kStep ? 0xFFFFFFFFu : (1u << have) - 1u;
+    uint32_t bits = have >= kStep ? 0xFFFFFFFFu : (1u << have) - 1u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (ev[h] == -INFINITY) bits &= h ? 0xFFFFu : 0xFFFF0000u;  // a page that is not there
+    const bool all = bits == 0xFFFFFFFFu;
     const uint32_t see[2] = {bits, bits};
     uint32_t pt[NR][2][2];
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr)
-      softmax(std::integral_constant<int, 2>(), nr, sc[nr], kmul, ev, have >= kStep, see, pt[nr]);
+      softmax(std::integral_constant<int, 2>(), nr, sc[nr], kmul, ev, all, see, pt[nr]);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       uint32_t v[4][D / 32];
@@ -387,6 +390,14 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
           v[i][0] = x.x;
           v[i][1] = x.y;
         }
+      }
+      if (!all) {  // codes outside the context may be anything, NaN too
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!((bits >> (half * kHalf + (i >> 1) * 8 + 2 * c + (i & 1))) & 1u)) {
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) v[i][w] = 0u;
+          }
       }
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {

@@ -1,7 +1,7 @@
 // attn_q8_wide.cu -- tree attention over the 8-bit key/value cache on the
 // tcgen05 tensor cores: d = 128 and more than 32 query rows per kv head.
 //
-// Mathematics: as in attn_q8.cu (codes as f16 of code * 2^-8, K exponents on
+// Mathematics: as in attn_q8.cu (codes as f16, K exponents on
 // the scores, V exponents in the softmax's reference, queries f16 under a power
 // of two per row); tree rows become f16 under a power of two per 16 rows.  P is
 // f16 too, so kind::f16 takes both products with f16 operands.
@@ -12,7 +12,7 @@
 // (A, B) of a kv head and KV tiles of 128 tokens, each converted once for both:
 //   * warpgroups 3 and 4 convert K and V: codes come from global memory into
 //     registers (the next tile's loads are issued as the last one's registers
-//     are used up), become f16 by integer instructions, and go to a ring of
+//     are used up), become f16, and go to a ring of
 //     two 32 KB slots each in the 128-byte swizzle that the MMAs read; tree
 //     rows likewise.  The codes never pass through a staging buffer, and any
 //     page size works, since no box has to fit a page;
@@ -44,7 +44,7 @@ constexpr int kTile = 2 * kHalfTile;         // 32 KB
 constexpr int kSlots = 4;
 constexpr float kSlack = 6.f;                // the reference moves when a score passes it by 2^6
 constexpr float kHead = 9.f;                 // P of a new maximum is 2^9: at most 2^15 in f16
-constexpr int kTreeTop = 4;                  // tree rows as f16: amax in [2^4, 2^5)
+constexpr int kTreeTop = 8;                  // tree rows as f16: amax in [2^8, 2^9), as large as codes
 constexpr int kGroup = 16;                   // tokens that share a place and an exponent
 constexpr int kGroups = BN / kGroup;
 constexpr int SN = 64;                       // tokens of a softmax step: half a KV tile
@@ -299,14 +299,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     for (int i = 0; go && i < nctx; ++i) {
       const int e = __shfl_sync(0xFFFFFFFFu, now.e, (i & 3) * 8 + (lane & 7));
       if (cw == 0) {
-        // what a K code * 2^-8 counts for; the V exponent of such a code
+        // what a K code counts for; the V exponent
         if (lane < kGroups) {
           if (kind == 0)
             sh->scales[i & 3][lane].x = e == kMissing ? 1.f : q8_scale(e);
           else
             sh->scales[i & 3][lane].y = e == kMissing ? -INFINITY
                                                       : e == DDT_Q8_EXP_NAN ? __int_as_float(0x7FC00000)
-                                                                            : (float)(q8_exp(e) + kCodeShift);
+                                                                            : (float)q8_exp(e);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->sc_full[i & 3]);
@@ -316,9 +316,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
       go = slot_free(i);
       if (!go) break;
       unsigned char* dst = sKV + slot_of(i) * kTile;
+      const int have = T - (t_lo + i) * BN;  // tokens of the tile, from here on
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const uint4 v = x[q];
+        uint4 v = x[q];
+        // V codes outside the context may be anything, NaN too (K's scores are masked)
+        if (kind && (q >> 1) * 32 + tok >= have) v = make_uint4(0, 0, 0, 0);
         if (i + 1 < nctx) load(now, i + 1, q);
         store(dst, (q >> 1) * 32 + tok, q & 1, make_uint4(codes_lo(v.x), codes_hi(v.x), codes_lo(v.y), codes_hi(v.y)),
               make_uint4(codes_lo(v.z), codes_hi(v.z), codes_lo(v.w), codes_hi(v.w)));

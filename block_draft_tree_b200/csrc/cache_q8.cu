@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(WriteParams p) {
         make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
   }
   if (e > e_old && older && !nan) {
-    const float down = pow2i(e_old - e + kCodeShift);
+    const float down = pow2i(e_old - e);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       if (!((older >> i) & 1u)) continue;
@@ -183,7 +183,7 @@ struct ReadParams {
 
 constexpr int kReadRows = 32;  // output rows of a CTA, at most
 
-// 8 codes -> 8 bf16; s: 2^(e + 8).
+// 8 codes -> 8 bf16; s: the block's scale.
 __device__ __forceinline__ uint4 decode8(uint2 c, float s) {
   const uint32_t w[2] = {c.x, c.y};
   uint32_t o[4];

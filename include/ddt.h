@@ -496,9 +496,9 @@ ddt_status ddt_tree_walk_sample(const void* logits, ddt_dtype dtype, int batch, 
 /* ------------------------------------------------------------------------
  * The 8-bit key/value cache.
  *
- * Codes: e4m3 (1 sign, 4 exponent, 3 fraction bits, largest value 448), one
- * byte per element in the layout of the bf16 cache; e4m3's NaN code
- * (S.1111.111) is never written and counts as +-480.  Scales: one int8
+ * Codes: e4m3 (1 sign, 4 exponent, 3 fraction bits, largest value 448;
+ * S.1111.111 is NaN and is never written here), one byte per element in the
+ * layout of the bf16 cache.  Scales: one int8
  * exponent e for every block of `block` tokens of every kv head, K and V
  * apart; an element's value is code * 2^e.  Exponents lie in
  * [DDT_Q8_EXP_MIN, DDT_Q8_EXP_MAX]; DDT_Q8_EXP_NAN marks a block that was

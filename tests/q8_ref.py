@@ -10,12 +10,12 @@ EXP_MIN, EXP_MAX, EXP_NAN = -48, 48, -128
 
 
 def code_values() -> torch.Tensor:
-    """f64 value of each of the 256 codes: e4m3, its NaN code counting as 480."""
+    """f64 value of each of the 256 e4m3 codes."""
     v = []
     for c in range(256):
         ex, fr = (c >> 3) & 15, c & 7
         m = fr * 2.0 ** -9 if ex == 0 else (8 + fr) * 2.0 ** (ex - 10)
-        v.append(-m if c & 128 else m)
+        v.append(math.nan if (c & 127) == 127 else (-m if c & 128 else m))
     return torch.tensor(v, dtype=torch.float64)
 
 

@@ -357,3 +357,15 @@ def test_waits_that_run_out_are_reported(n, page):
     finally:
         api.set_wait_limit(0)
     c.go()
+
+
+def test_nan_codes_in_the_context():
+    """A NaN code that someone else wrote: in K every row of its head is NaN, in
+    V that one column."""
+    for n in (1, 70, 140):
+        c = Case(n, 4, 2, 128, ctx=(50, 60), seed=n)
+        c.c.codes[0][0, 17, 1, 3] = 0x7F
+        c.c.codes[1][1, 18, 0, 4] = 0xFF
+        out, _ = c.run()
+        assert out[0, :, 2:].isnan().all() and not out[0, :, :2].isnan().any()
+        assert out[1, :, :2, 4].isnan().all() and out[1].isnan().sum() == n * 2

@@ -182,7 +182,7 @@ def test_reference_codes_are_torchs_e4m3():
     codes = torch.arange(256, dtype=torch.uint8)
     want = codes.view(torch.float8_e4m3fn).double()
     got = q8_ref.decode(codes)
-    assert torch.equal(got[~want.isnan()], want[~want.isnan()]) and want.isnan().sum() == 2
+    assert torch.equal(got.nan_to_num(1e9), want.nan_to_num(1e9)) and want.isnan().sum() == 2
     v = q8_ref.code_values()[:127]
     mid = (v[1:] + v[:-1]) / 2
     y = torch.cat([v, mid, mid * (1 + 2.0 ** -20), mid * (1 - 2.0 ** -20)])
