@@ -9,7 +9,7 @@
 // running bound on t_j, P_j = 2^(t_j - m) weighs the bare codes and the
 // denominator adds P_j 2^-e_j.  So the codes meet the tensor cores as f16
 // (exact: e4m3 is a subset of f16), scales cost one multiply-add per score,
-// and P as f16 (11 bits, error 2^-12) keeps every block's share whatever its
+// and P as f16 (11 bits, error 2^-11) keeps every block's share whatever its
 // scale.  m lags the true maximum by up to 2^4 and P's range begins at 2^11 for
 // a new maximum: weights reach 2^15 at most, and f16's subnormal step (2^-24)
 // is 2^-35 of the maximum, below any sum over a long tail.  Queries become f16

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(WriteParams p) {
   const uint4* src = (kv ? p.v_new : p.k_new) + ((int64_t)b * p.n_max * hkv + h) * CH + tu % CH;
   uint4 x[NP];
   uint32_t fresh = 0, older = 0;  // bit i: pass i holds a new row / an older code
-  uint32_t amax = 0;  // the largest magnitude's bits
+  uint32_t amax = 0;  // the largest magnitudes' bits, of even and odd elements
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int64_t pos = pos0 + tu / CH + i * RP;
@@ -112,9 +112,9 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(WriteParams p) {
   const int e_old = q8_exp(e_was);
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    amax = max(amax, max(max_bf16(x[i].x), max_bf16(x[i].y)));
-    amax = max(amax, max(max_bf16(x[i].z), max_bf16(x[i].w)));
+    amax = max_bf16x2(max_bf16x2(max_bf16x2(max_bf16x2(amax, x[i].x), x[i].y), x[i].z), x[i].w);
   }
+  amax = max_bf16(amax);
   // bit 31: some row is new (so that an all-zero block still gets its exponent)
   amax = __reduce_max_sync(0xFFFFFFFFu, amax | (fresh ? 0x80000000u : 0u));
   if (TU > 32) {
@@ -139,7 +139,9 @@ __global__ void __launch_bounds__(kThreads) write_q8_kernel(WriteParams p) {
     uint32_t c[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      c[q] = nan ? 0u : f32x2_to_e4m3x2(bf16_lo(w[q]) * inv, bf16_hi(w[q]) * inv);
+      float lo, hi;
+      unpack2(fmul2(pack2(bf16_lo(w[q]), bf16_hi(w[q])), pack2(inv, inv)), lo, hi);
+      c[q] = nan ? 0u : f32x2_to_e4m3x2(lo, hi);
     }
     *(uint2*)(codes + (int64_t)(tu / CH + i * RP) * hkv * D) =
         make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
@@ -190,8 +192,11 @@ __device__ __forceinline__ uint4 decode8(uint2 c, float s) {
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const float2 a = f16x2_to_f32x2(codes_lo(w[q])), z = f16x2_to_f32x2(codes_hi(w[q]));
-    o[2 * q] = f32x2_to_bf16x2(a.x * s, a.y * s);
-    o[2 * q + 1] = f32x2_to_bf16x2(z.x * s, z.y * s);
+    float b[4];
+    unpack2(fmul2(pack2(a.x, a.y), pack2(s, s)), b[0], b[1]);
+    unpack2(fmul2(pack2(z.x, z.y), pack2(s, s)), b[2], b[3]);
+    o[2 * q] = f32x2_to_bf16x2(b[0], b[1]);
+    o[2 * q + 1] = f32x2_to_bf16x2(b[2], b[3]);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -217,28 +222,35 @@ __global__ void __launch_bounds__(kThreads) read_q8_kernel(ReadParams p) {
   __syncthreads();
   pdl_trigger();
   const int vecs = p.c.hkv * p.c.d / 8;  // 8-code vectors of a row: a warp writes 512 bytes in a row
-  const int per_head = p.c.d / 8;
+  const int head_log2 = p.c.d == 128 ? 4 : 3;
   const uint2* codes = (const uint2*)(kv ? p.c.vc : p.c.kc);
   const int8_t* exps = kv ? p.c.ve : p.c.ke;
   const int rows = min(p.rows, p.n_max - r0);
   const int items = rows * vecs;
   uint4* out = (kv ? p.v_out : p.k_out) + ((int64_t)b * p.n_max + r0) * vecs;
   constexpr int kFly = 8;  // vectors in flight per thread
+  // item i = row r, vector x of it, stepped without divisions
+  const int dr = kThreads / vecs, dx = kThreads % vecs;
+  int r = tid / vecs, x = tid % vecs;
   for (int i0 = tid; i0 < items; i0 += kThreads * kFly) {
     uint2 v[kFly];
     int e[kFly];
 #pragma unroll
     for (int q = 0; q < kFly; ++q) {
-      const int i = i0 + q * kThreads;
       v[q] = make_uint2(0, 0);
       e[q] = 0;
-      if (i < items) {
-        const int r = i / vecs, x = i - r * vecs;
+      if (r < rows) {
         const Q8Place at = s_at[r];
         if (at.row >= 0) {
           v[q] = __ldcs(codes + at.row * vecs + x);
-          e[q] = __ldg(exps + at.blk * p.c.hkv + x / per_head);
+          e[q] = __ldg(exps + at.blk * p.c.hkv + (x >> head_log2));
         }
+      }
+      r += dr;
+      x += dx;
+      if (x >= vecs) {
+        x -= vecs;
+        ++r;
       }
     }
 #pragma unroll

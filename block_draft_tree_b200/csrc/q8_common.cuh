@@ -101,6 +101,8 @@ __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) {
 
 // The larger magnitude's bits of two packed bf16.
 __device__ __forceinline__ uint32_t max_bf16(uint32_t w) { return max(w & 0x7FFFu, (w >> 16) & 0x7FFFu); }
+// Magnitude bits of packed bf16 pairs, half by half.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
 // The larger magnitude bits of the finite ones among two packed bf16 and m.
 __device__ __forceinline__ uint32_t max_finite_bf16(uint32_t m, uint32_t w) {
   const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;

@@ -617,7 +617,7 @@ ddt_status ddt_kv_read_q8(const ddt_kv_read_q8_args* a, cudaStream_t stream);
  * with mask bit 0 set is an ordinary decoding step.  Scores, softmax sums and
  * outputs accumulate in fp32; queries, codes and softmax weights meet the
  * tensor cores as f16 under power-of-two scales (codes exactly, a query
- * element to 2^-39 of its row's largest, a weight to 2^-12).  Tree K/V rows
+ * element to 2^-39 of its row's largest, a weight to 2^-11).  Tree K/V rows
  * hold magnitudes up to 2^56; larger ones may count as infinities.  A
  * non-finite tree value reaches only the rows whose mask shows it.  A page id
  * outside the pool below ctx_len raises DDT_ERR_INVALID_ARG in dev_status and

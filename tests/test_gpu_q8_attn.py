@@ -269,9 +269,10 @@ def test_agrees_with_the_bf16_attention_over_the_read_back_cache():
         assert (lse - l2).abs().max() <= 1e-3
 
 
-def test_two_streams_and_two_graphs_at_once():
+@pytest.mark.parametrize("n", [1, 70])
+def test_two_streams_and_two_graphs_at_once(n):
     """Calls in flight together, eager and captured, each with its own scratch."""
-    cs = [Case(1, 8, 1, 128, ctx=(4096,), seed=s) for s in (1, 2)]
+    cs = [Case(n, 8, 1, 128, ctx=(4096,), seed=s) for s in (1, 2)]
     masks = [_pack(c.see) for c in cs]
     nn, cl = [_i32(c.n_nodes) for c in cs], [_i32(c.ctx) for c in cs]
 
