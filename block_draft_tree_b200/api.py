@@ -796,9 +796,9 @@ def _status_q8(fn: str, t):
 
 def _call_q8(name: str, args, dev: int):
     """The entry point ``name`` on device ``dev`` (made current) and its current stream."""
-    f = getattr(load_library(), name)
+    f = getattr(_lib or load_library(), name)
     stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         rc = f(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -946,11 +946,12 @@ def tree_attn_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
         a.lse_out = lse.data_ptr()
     ref = ctypes.byref(a)
-    if torch.cuda.current_device() == dev:
-        nb = load_library().ddt_tree_attn_q8_workspace_size(ref)
+    lib = _lib or load_library()
+    if torch._C._cuda_getDevice() == dev:
+        nb = lib.ddt_tree_attn_q8_workspace_size(ref)
     else:
         with torch.cuda.device(dev):
-            nb = load_library().ddt_tree_attn_q8_workspace_size(ref)
+            nb = lib.ddt_tree_attn_q8_workspace_size(ref)
     # scratch of this call alone: calls on other streams and captured graphs have their own
     ws = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
     _call_q8("ddt_tree_attn_q8", (ref, ws.data_ptr() if nb else None, nb), dev)
