@@ -28,6 +28,9 @@
 // fragments; for V, lane (g, c) holds tokens 2c, 2c+1, 8+2c, 9+2c and chunk g,
 // whose pairs one byte permute interleaves for the conversion to f16;
 // P^T turns between the products by movmatrix.
+// Measured: one row of 32 ragged sequences of 1024 .. 32768 tokens, 32/8 heads,
+// 64-token pages, 190 us = 5.8 TB/s, 0.88 of the copy rate; 4 x 131072 tokens,
+// 16/1 heads, 37 us with the merge of 111 splits.
 #include <algorithm>
 #include <type_traits>
 
@@ -52,7 +55,10 @@ constexpr int kHalf = 16;              // tokens that share a place and an expon
 constexpr int kStep = 2 * kHalf;       // tokens of a step
 constexpr float kSlack = 4.f;          // the reference moves when a score passes it by 2^4
 constexpr float kHead = 11.f;          // P of a new maximum is 2^11
-constexpr long kWideRows = 32;         // rows per kv head beyond which d = 128 takes the wide kernel
+// Rows per kv head beyond which d = 128 takes the wide kernel (4 x 16384 tokens:
+// 40 rows 80 us there and 103 us here, 80 rows 83 us and 141 us; 20 x 2736 tokens:
+// 111 us and 75 us, 115 us and 136 us; up to 32 rows are one pass here).
+constexpr long kWideRows = 32;
 constexpr int kTreeTop = 8;            // tree rows as f16: amax in [2^8, 2^9), as large as codes
 
 // D += A (16x16, row) * B (16x8, col), f16 inputs, f32 accumulators.
@@ -742,7 +748,9 @@ Plan plan_of(const ddt_attn_q8_args* a) {
   const long steps = (a->max_ctx + kStep - 1) / kStep + (a->n_max + kHalf - 1) / kHalf;
   const long slots = (long)device_sm_count() * (pl.nr <= 2 ? 3 : 2);
   // as many splits as fill the device, of at least 2 steps a warp; long
-  // contexts in splits of at most kLong steps, so that ragged ones even out
+  // contexts in splits of at most kLong steps, so that ragged ones even out (32
+  // ragged sequences: 564 us in one split each; 40 to 128 steps are alike, 32
+  // would cut 4 x 131072 tokens into more than one wave: 50 us against 37 us)
   constexpr long kLong = 64;
   long ns = std::max(1L, slots / std::max(1L, base));
   ns = std::min(ns, std::max(1L, steps / (2 * kWarps)));

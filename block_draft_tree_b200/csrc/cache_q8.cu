@@ -14,7 +14,10 @@
 // and one of 128 takes a CTA), loaded once, reduced to amax, converted and
 // stored: each input byte is read once and each code written once, which is
 // what bounds a prompt (3 bytes per element); a single token is a launch's
-// latency.
+// latency.  Measured: 4 prompts of up to 8192 tokens, 8 heads of 128, written
+// and read back in 63 us (0.85 of the copy rate), 8 contexts of up to 32768
+// tokens read in 211 us (the copy rate); both were bound by their issue slots
+// (80 us, 232 us) until magnitudes and multiplies went two at a time.
 #include "launch.h"
 #include "q8_common.cuh"
 
