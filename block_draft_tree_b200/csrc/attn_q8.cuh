@@ -54,6 +54,17 @@ __device__ __forceinline__ int group_of(const AttnQ8Params& p, int z, int* s_pic
   return *s_pick * p.c.hkv + z % p.c.hkv;
 }
 
+// What a converter thread of the wide kernel reads of KV tile `tile` (128 tokens)
+// in pass q (0..7): token 32 (q / 2) + tok, tok < 32, of the tile.  Rows behind the
+// context are never touched: a cache's length need not be a multiple of 16, so
+// they may lie past its end.  left: the context's tokens from the thread's
+// first one on; group_row: the first cache row of the token's group of 16 (-1: a
+// page that is not there, or nothing of the context).
+__host__ __device__ constexpr int q8_wide_left(int T, int tile, int tok) { return T - tile * 128 - tok; }
+__host__ __device__ constexpr bool q8_wide_reads(int group_row, int q, int left) {
+  return group_row >= 0 && (q >> 1) * 32 < left;
+}
+
 Q8View q8_view(const ddt_q8_cache* c);
 
 }  // namespace ddt

@@ -248,14 +248,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     const uint32_t stride = (uint32_t)p.c.hkv * D;
     const int nctx = min(max(nct - t_lo, 0), ntiles);  // context tiles of this CTA
     // places and exponents of the 16-token groups of 4 tiles, a group a lane; a
-    // group that is not there reads row 0 and weighs nothing
+    // group that is not there (row -1) is zeros and weighs nothing
     struct LookUp {
       int row, e;
     };
     constexpr int kMissing = 1 << 16;  // exponent of a group that is not there
     const int8_t* exps = kind ? p.c.ve : p.c.ke;
     auto look_up = [&](int i) -> LookUp {  // of tiles i .. i + 3
-      LookUp u{0, kMissing};
+      LookUp u{-1, kMissing};
       const int64_t pos = ((int64_t)(t_lo + i) * kGroups + lane) * kGroup;
       if (i + (lane >> 3) < nctx && pos < T) {
         const Q8Place at = q8_place(p.c, b, pos);
@@ -269,13 +269,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
       return u;
     };
     // codes of the next tile to convert: pass q holds slice q & 1 of tokens
-    // 32 (q / 2) + tok, of group 2 (q / 2) + (cw >= 2)
+    // 32 (q / 2) + tok, of group 2 (q / 2) + (cw >= 2); what is not in the context
+    // is neither read nor anything but 0 (codes there may be anything, NaN too)
     uint4 x[8];
     const uint8_t* lane_src =
         (kind ? p.c.vc : p.c.kc) + (int64_t)kvh * D + (tok & 15) * (int64_t)stride + c4 * 16;
-    auto load = [&](const LookUp& u, int i, int q) {
+    auto load = [&](const LookUp& u, int i, int q, int left) {
       const int r = __shfl_sync(0xFFFFFFFFu, u.row, (i & 3) * 8 + (q >> 1) * 2 + (cw >> 1));
-      x[q] = ld_stream_v4(lane_src + (uint64_t)(uint32_t)r * stride + (q & 1) * 64);
+      x[q] = ld_stream_v4_if(lane_src + (uint64_t)(uint32_t)r * stride + (q & 1) * 64,
+                             q8_wide_reads(r, q, left));
     };
     // 16 elements as f16 to their two chunks of row r (of rows of two parities
     // a quarter warp writes, the swizzle gives eight different banks)
@@ -297,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     if (nctx > 0) {
       now = look_up(0);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) load(now, 0, q);
+      for (int q = 0; q < 8; ++q) load(now, 0, q, q8_wide_left(T, t_lo, tok));
     }
     for (int i = 0; go && i < nctx; ++i) {
       const int e = __shfl_sync(0xFFFFFFFFu, now.e, (i & 3) * 8 + (lane & 7));
@@ -319,13 +321,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
       go = slot_free(i);
       if (!go) break;
       unsigned char* dst = sKV + slot_of(i) * kTile;
-      const int have = T - (t_lo + i) * BN;  // tokens of the tile, from here on
+      const int left = q8_wide_left(T, t_lo + i + 1, tok);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        uint4 v = x[q];
-        // V codes outside the context may be anything, NaN too (K's scores are masked)
-        if (kind && (q >> 1) * 32 + tok >= have) v = make_uint4(0, 0, 0, 0);
-        if (i + 1 < nctx) load(now, i + 1, q);
+        const uint4 v = x[q];
+        if (i + 1 < nctx) load(now, i + 1, q, left);
         store(dst, (q >> 1) * 32 + tok, q & 1, make_uint4(codes_lo(v.x), codes_hi(v.x), codes_lo(v.y), codes_hi(v.y)),
               make_uint4(codes_lo(v.z), codes_hi(v.z), codes_lo(v.w), codes_hi(v.w)));
       }

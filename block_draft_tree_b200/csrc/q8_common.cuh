@@ -99,6 +99,18 @@ __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// ld_stream_v4 where `there`, zeros (and no access) elsewhere.
+__device__ __forceinline__ uint4 ld_stream_v4_if(const void* p, bool there) {
+  uint4 r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+      : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
+      : "l"(p), "r"((uint32_t)there));
+  return r;
+}
+
 // The larger magnitude's bits of two packed bf16.
 __device__ __forceinline__ uint32_t max_bf16(uint32_t w) { return max(w & 0x7FFFu, (w >> 16) & 0x7FFFu); }
 // Magnitude bits of packed bf16 pairs, half by half.
