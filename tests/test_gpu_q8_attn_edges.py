@@ -1,13 +1,48 @@
 """Tree attention over the 8-bit cache where its surroundings are hostile:
-caches that end inside a tile with NaN codes around them.  Reference and
+pages that are not there beside pages of NaN codes, caches that end inside a
+tile with NaN codes around them.  Reference and
 tolerance are those of test_gpu_q8_attn."""
 import pytest
 import torch
 
+import q8_ref
 from test_gpu_q8_attn import Case
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+
+
+def _leave_out_missing(c: Case):
+    """The reference without the positions whose page is not there."""
+    pool = c.c.codes[0].shape[0]
+
+    def values(which, i, n):
+        codes, exps = c.c.codes[which], q8_ref.scales(c.c.exps[which])
+        t = torch.arange(n, device=DEV)
+        pg = c.c.page_table[i].long()[t // c.c.page]
+        t, pg = t[(pg >= 0) & (pg < pool)], pg[(pg >= 0) & (pg < pool)]
+        slot = t % c.c.page
+        return q8_ref.decode(codes[pg, slot]) * exps[pg, slot // c.c.block][:, :, None]
+
+    c.c.values = values
+
+
+@pytest.mark.parametrize("n,hq", [(1, 4), (9, 4), (70, 4), (140, 8)])
+@pytest.mark.parametrize("page", [16, 48, 64])
+def test_tokens_of_missing_pages_are_left_out(n, hq, page):
+    """Page ids below and beyond the pool, at the start, inside and at the end of
+    a context, and a sequence with no page at all; the pool's first page, which
+    belongs to nobody, holds NaN codes."""
+    c = Case(n, hq, 1, 128, page=page, ctx=(130, 100, 2 * page, 500), seed=n + page)
+    pt = c.c.page_table
+    spare = next(p for p in range(c.c.codes[0].shape[0]) if p not in pt.flatten().tolist())
+    pt[pt == 0] = spare
+    for w in range(2):
+        c.c.codes[w][0] = 0x7F
+        c.c.exps[w][0] = 48
+    pt[0, 1], pt[1, 0], pt[2], pt[3, 2], pt[3, 500 // page] = -1, 1 << 30, -7, c.c.codes[0].shape[0], -1
+    _leave_out_missing(c)
+    c.check(*c.run(), status=1)
 
 
 @pytest.mark.parametrize("n,hq", [(1, 8), (70, 1), (140, 2)])
