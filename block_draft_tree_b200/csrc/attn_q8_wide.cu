@@ -610,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
               make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
       }
     }
+    __syncwarp();  // lanes read one another's rows from here on (a vote orders no memory)
     const uint32_t write_rows = __ballot_sync(0xFFFFFFFFu, writes && !final_out);
     if (write_rows) {
       float* dst = p.part_o + (part0 + qr0) * D + 4 * lane;

@@ -57,3 +57,17 @@ def test_caches_that_end_inside_a_tile(n, hq):
             inner.copy_(x)
             c.c.codes[w] = inner
         c.go()
+
+
+def test_split_trees_with_non_finite_rows_repeat_to_the_bit():
+    """Splits of a large tree whose lanes take different ways through the
+    epilogue (rows that see non-finite values and rows that do not)."""
+    c = Case(70, 8, 2, 128, ctx=(6000, 77), seed=5)
+    c.vt[0, 3, 0, 5], c.vt[0, 40, 1, 100] = float("inf"), float("nan")
+    first = c.run()
+    c.check(*first)
+    for _ in range(10):
+        again = c.run()
+        for x, y in zip(first, again):
+            assert torch.equal(x.view(torch.int16 if x.dtype == torch.bfloat16 else torch.int32),
+                               y.view(torch.int16 if y.dtype == torch.bfloat16 else torch.int32))
