@@ -87,12 +87,6 @@ __device__ __forceinline__ int f16_exponent(uint32_t amax_bits, int top) {
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float inv) {
   return f32x2_to_f16x2(bf16_lo(w) * inv, bf16_hi(w) * inv);
 }
-// Same, non-finite elements as 0.
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2_finite(uint32_t w, float inv) {
-  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
-  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
-  return bf16x2_to_f16x2(w, inv);
-}
 
 template <int D, int NR>
 struct Smem {
@@ -481,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
     // V: tokens 2c, 2c+1, 8+2c, 9+2c, elements g*D/8 ..
     uint32_t v[4][D / 16];
     uint32_t vmax = 0;
-    bool odd = false;  // a non-finite element
+    bool odd = false;  // a wild element
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = (i >> 1) * 8 + 2 * c + (i & 1);
@@ -492,9 +486,9 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t w = word(x, e);
-          vmax = max_finite_bf16(vmax, w);
-          odd |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-          v[i][q * 4 + e] = w;
+          odd |= has_wild(w);
+          v[i][q * 4 + e] = tame_bf16x2(w);
+          vmax = max(vmax, max_bf16(v[i][q * 4 + e]));
         }
       }
     }
@@ -515,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
       }
       softmax(std::integral_constant<int, 1>(), nr, sc[nr], &kmul, &evf, false, see, pt[nr]);
       if (odd) {
-        // a non-finite V element reaches the rows that see its token, and no others
+        // a wild V element reaches the rows that see its token, and no others
         for (int t = 0; t < cnt; ++t)
 #pragma unroll
           for (int r = 0; r < 2; ++r)
@@ -525,15 +519,15 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const uint16_t x = vt[t * stride + g * (D / 8) + 2 * i + e];
-                  if ((x & 0x7F80u) == 0x7F80u) o[nr][i][2 * e + r] += bf16_to_f32(x);
+                  if (is_wild(x)) o[nr][i][2 * e + r] += wild_value(x);
                 }
             }
       }
     }
 #pragma unroll
     for (int w = 0; w < NT; ++w) {
-      const uint32_t x0 = bf16x2_to_f16x2_finite(v[0][w], vinv), x1 = bf16x2_to_f16x2_finite(v[1][w], vinv);
-      const uint32_t y0 = bf16x2_to_f16x2_finite(v[2][w], vinv), y1 = bf16x2_to_f16x2_finite(v[3][w], vinv);
+      const uint32_t x0 = bf16x2_to_f16x2(v[0][w], vinv), x1 = bf16x2_to_f16x2(v[1][w], vinv);
+      const uint32_t y0 = bf16x2_to_f16x2(v[2][w], vinv), y1 = bf16x2_to_f16x2(v[3][w], vinv);
       const uint32_t a[4] = {prmt(x0, x1, 0x5410), prmt(x0, x1, 0x7632), prmt(y0, y1, 0x5410),
                              prmt(y0, y1, 0x7632)};
 #pragma unroll

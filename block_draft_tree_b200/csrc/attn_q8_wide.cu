@@ -63,7 +63,7 @@ struct __align__(16) Shared {
   int abort, pick;
   float2 scales[4][kGroups];  // (what a K product counts for, V exponent)
   uint32_t amax[2][2][kGroups];  // K, V: largest magnitudes of a tree tile's groups, from two warps each
-  uint32_t odd[32];           // tree rows with a non-finite V element
+  uint32_t odd[32];           // tree rows with a wild V element
 };
 
 __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, Shared* sh) {
@@ -357,12 +357,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
           bool odd = false;
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            const uint4 v = w[2 * q + (h >> 1)][h & 1];
+            uint4& v = w[2 * q + (h >> 1)][h & 1];
+            if (kind) {  // wild V elements go to their rows at the end, and to no others
+              odd |= has_wild(v.x) || has_wild(v.y) || has_wild(v.z) || has_wild(v.w);
+              v = make_uint4(tame_bf16x2(v.x), tame_bf16x2(v.y), tame_bf16x2(v.z), tame_bf16x2(v.w));
+            }
             m = max_finite_bf16(max_finite_bf16(max_finite_bf16(max_finite_bf16(m, v.x), v.y), v.z), v.w);
-            odd |= max(max(max_bf16(v.x), max_bf16(v.y)), max(max_bf16(v.z), max_bf16(v.w))) >= 0x7F80u;
           }
           const int tr = row0 + half * 64 + q * 32 + tok;
-          if (odd && kind) atomicOr(&sh->odd[tr >> 5], 1u << (tr & 31));
+          if (odd) atomicOr(&sh->odd[tr >> 5], 1u << (tr & 31));
           m = __reduce_max_sync(0xFFFFFFFFu, m);
           if (lane == 0) sh->amax[kind][cw & 1][half * 4 + 2 * q + (cw >> 1)] = m;
         }
@@ -390,13 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
           for (int h = 0; h < 2; ++h) {
             uint32_t u[4] = {w[q][h].x, w[q][h].y, w[q][h].z, w[q][h].w};
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              if (kind) {  // non-finite V elements go to their rows at the end, and to no others
-                if ((u[z] & 0x7F80u) == 0x7F80u) u[z] &= 0xFFFF0000u;
-                if ((u[z] & 0x7F800000u) == 0x7F800000u) u[z] &= 0x0000FFFFu;
-              }
-              u[z] = bf16x2_to_f16x2(u[z], inv);
-            }
+            for (int z = 0; z < 4; ++z) u[z] = bf16x2_to_f16x2(u[z], inv);
             f[h] = make_uint4(u[0], u[1], u[2], u[3]);
           }
           store(dst, half * 64 + (q >> 1) * 32 + tok, q & 1, f[0], f[1]);
@@ -574,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0u;
       } else if (t_hi > nct) {
-        // non-finite V elements of the tree rows that this row sees, in this CTA's tiles
+        // wild V elements of the tree rows that this row sees, in this CTA's tiles
         const int w_lo = max(t_lo - nct, 0) * 4, w_hi = min((t_hi - nct) * 4, p.W);
 #pragma unroll 1
         for (int w = w_lo; w < w_hi; ++w) {
@@ -587,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const uint16_t z = v[e];
-              if ((z & 0x7F80u) == 0x7F80u) o[e] = __float_as_uint(__uint_as_float(o[e]) + bf16_to_f32(z));
+              if (is_wild(z)) o[e] = __float_as_uint(__uint_as_float(o[e]) + wild_value(z));
             }
           }
         }

@@ -123,4 +123,23 @@ __device__ __forceinline__ uint32_t max_finite_bf16(uint32_t m, uint32_t w) {
   return m;
 }
 
+
+// Tree V values from 2^57 on, infinities and NaN are no operands of the
+// products, where even a weight of 0 would make NaN of them: they count as 0
+// there, and as infinities (or NaN) in the rows whose mask shows them.
+constexpr uint32_t kWildBits = (127 + 57) << 7;  // magnitude bits of bf16 2^57
+__device__ __forceinline__ bool is_wild(uint32_t bf16_bits) { return (bf16_bits & 0x7FFFu) >= kWildBits; }
+__device__ __forceinline__ bool has_wild(uint32_t w) { return is_wild(w) || is_wild(w >> 16); }
+// Two packed bf16, wild ones as 0.
+__device__ __forceinline__ uint32_t tame_bf16x2(uint32_t w) {
+  if (is_wild(w)) w &= 0xFFFF0000u;
+  if (is_wild(w >> 16)) w &= 0x0000FFFFu;
+  return w;
+}
+// What a wild value counts for where it is seen.
+__device__ __forceinline__ float wild_value(uint32_t bf16_bits) {
+  return (bf16_bits & 0x7FFFu) > 0x7F80u ? __int_as_float(0x7FC00000)
+                                         : (bf16_bits & 0x8000u) ? -INFINITY : INFINITY;
+}
+
 }  // namespace ddt

@@ -1,6 +1,6 @@
 """Tree attention over the 8-bit cache where its surroundings are hostile:
 pages that are not there beside pages of NaN codes, caches that end inside a
-tile with NaN codes around them.  Reference and
+tile with NaN codes around them, tree rows out of all proportion.  Reference and
 tolerance are those of test_gpu_q8_attn."""
 import pytest
 import torch
@@ -71,3 +71,18 @@ def test_split_trees_with_non_finite_rows_repeat_to_the_bit():
         for x, y in zip(first, again):
             assert torch.equal(x.view(torch.int16 if x.dtype == torch.bfloat16 else torch.int32),
                                y.view(torch.int16 if y.dtype == torch.bfloat16 else torch.int32))
+
+
+@pytest.mark.parametrize("n,d", [(2, 128), (9, 64), (9, 128), (70, 128), (140, 128)])
+def test_huge_tree_values_reach_only_those_who_see_them(n, d):
+    """V values from 2^57 on count as infinities where they are seen and as
+    nothing elsewhere, also beside ordinary values of the same 16 rows."""
+    c = Case(n, 4, 1, d, ctx=(50, 0), seed=n)
+    c.vt[1, n - 1, 0, 0] = -2.0 ** 57
+    c.vt[0, n - 1] = 3e38
+    if n > 6:
+        c.vt[0, 5, 0, 7], c.vt[0, 6, 0, 8:12] = 1e30, -1e25
+    out, lse = c.run()
+    huge = c.vt.abs() >= 2.0 ** 57
+    c.vt = torch.where(huge, c.vt * float("inf"), c.vt)
+    c.check(out, lse)
