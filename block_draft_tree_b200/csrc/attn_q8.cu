@@ -275,14 +275,15 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
 #pragma unroll
       for (int h = 1; h < NH; ++h) top[r] = fmax3(top[r], sc[h][r], sc[h][2 + r]);
     }
-    if (__any_sync(0xFFFFFFFFu, top[0] > m_ref[nr][0] + (kSlack + kHead) || top[1] > m_ref[nr][1] + (kSlack + kHead))) {
+    // (differences: where scores are so large that their last place is above 1, a sum would round past f16's range)
+    if (__any_sync(0xFFFFFFFFu, top[0] - m_ref[nr][0] > kSlack + kHead || top[1] - m_ref[nr][1] > kSlack + kHead)) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], x));
         float alpha = 1.f;
-        if (top[r] > m_ref[nr][r] + (kSlack + kHead)) {
-          const float to = top[r] - kHead;
+        if (top[r] - m_ref[nr][r] > kSlack + kHead) {
+          const float to = reference_below(top[r], kHead, kSlack);
           alpha = m_ref[nr][r] == -INFINITY ? 0.f : ex2(m_ref[nr][r] - to);
           m_ref[nr][r] = to;
         }

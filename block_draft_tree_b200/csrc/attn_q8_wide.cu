@@ -47,6 +47,7 @@ constexpr int kTile = 2 * kHalfTile;         // 32 KB
 constexpr int kSlots = 4;
 constexpr float kSlack = 6.f;                // the reference moves when a score passes it by 2^6
 constexpr float kHead = 9.f;                 // P of a new maximum is 2^9: at most 2^15 in f16
+constexpr float kFar = 1048576.f;            // references from here on have a last place of 2^-3 and more
 constexpr int kTreeTop = 8;                  // tree rows as f16: amax in [2^8, 2^9), as large as codes
 constexpr int kGroup = 16;                   // tokens that share a place and an exponent
 constexpr int kGroups = BN / kGroup;
@@ -490,13 +491,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
         top = fmaxf(top, fmaf(fmaxf(m2[0], m2[1]), f[q], ev[q]));
       }
       float alpha = 1.f;
-      const bool move = top > m_ref + (kSlack + kHead);
+      const bool move = top - m_ref > kSlack + kHead;
       if (move) {
-        alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - (top - kHead));
-        m_ref = top - kHead;
+        const float to = reference_below(top, kHead, kSlack);
+        alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - to);
+        m_ref = to;
         l *= alpha;
       }
       const float m = m_ref == -INFINITY ? 0.f : m_ref;
+      float c_of[SN / kGroup];  // P = 2^(f s + c)
+#pragma unroll
+      for (int q = 0; q < SN / kGroup; ++q) c_of[q] = ev[q] - m;
+      if (__any_sync(0xFFFFFFFFu, fabsf(m) > kFar)) {
+        // t rounded first, as its maximum was: in one fma with m, P could pass f16's range
+#pragma unroll
+        for (int q = 0; q < SN / kGroup; ++q) {
+#pragma unroll
+          for (int e = 0; e < kGroup; ++e)
+            r[16 * q + e] = __float_as_uint(fmaf(__uint_as_float(r[16 * q + e]), f[q], ev[q]) - m);
+          f[q] = 1.f;
+          c_of[q] = 0.f;
+        }
+      }
       // P = 2^(t - m) as f16 pairs over the scores, its sum weighted by 2^-(V
       // exponent).  (A quarter of the 2^x on the FMA pipe instead of MUFU gave
       // 1 %, more of them lost: the issue slots are as scarce.)
@@ -506,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int gq = 2 * c + q;
-          const uint64_t f2 = pack2(f[gq], f[gq]), c2 = pack2(ev[gq] - m, ev[gq] - m);
+          const uint64_t f2 = pack2(f[gq], f[gq]), c2 = pack2(c_of[gq], c_of[gq]);
           uint64_t s2[2] = {0ull, 0ull};
 #pragma unroll
           for (int e = 0; e < kGroup; e += 2) {

@@ -99,6 +99,14 @@ __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// The softmax's reference for a largest exponent `top`: top - head, or top itself
+// where the difference does not come out within head + slack of it (|top| beyond
+// 2^26, whose last place is 8 and more), so that 2^(top - reference) fits f16.
+__device__ __forceinline__ float reference_below(float top, float head, float slack) {
+  const float to = top - head;
+  return top - to <= head + slack ? to : top;
+}
+
 // ld_stream_v4 where `there`, zeros (and no access) elsewhere.
 __device__ __forceinline__ uint4 ld_stream_v4_if(const void* p, bool there) {
   uint4 r;

@@ -1,6 +1,6 @@
 """Tree attention over the 8-bit cache where its surroundings are hostile:
 pages that are not there beside pages of NaN codes, caches that end inside a
-tile with NaN codes around them, tree rows out of all proportion.  Reference and
+tile with NaN codes around them, tree rows out of all proportion, scores of any size.  Reference and
 tolerance are those of test_gpu_q8_attn."""
 import pytest
 import torch
@@ -86,3 +86,42 @@ def test_huge_tree_values_reach_only_those_who_see_them(n, d):
     huge = c.vt.abs() >= 2.0 ** 57
     c.vt = torch.where(huge, c.vt * float("inf"), c.vt)
     c.check(out, lse)
+
+
+@pytest.mark.parametrize("n", [1, 9, 70, 140])
+def test_scores_of_any_size(n):
+    """Scores up to 2^50, whose last place is far above 1: tokens of the same
+    largest score share the row (K and Q have one channel each, so that scores are
+    exact), and sums of many channels stay within what is attended to."""
+    for p in range(10, 64, 1):
+        c = Case(n, 2, 1, 128, ctx=(300, 0), seed=n, exps=(-6, -6))
+        c.scale = 0.125
+        g = torch.Generator().manual_seed(p)
+        ch = torch.tensor([0x38, 0x30, 0xB8], dtype=torch.uint8)      # 1, 1/2, -1 times 2^-6
+        c.c.codes[0].zero_()
+        c.c.codes[0][0, :, 0, 0] = ch[torch.randint(0, 3, (300,), generator=g)].to(DEV)
+        c.c.codes[0][0, 0, 0, 0] = 0x38
+        c.q.zero_()
+        c.q[..., 0] = 2.0 ** p
+        c.kt.zero_()
+        c.kt[0, :, 0, 0] = 2.0 ** -8
+        c.kt[1, :, 0, 0] = torch.tensor([1.0, 0.5])[torch.randint(0, 2, (n,), generator=g)].to(torch.bfloat16).to(DEV)
+        c.vt = torch.where(c.vt < 0, -1.0, 1.0).to(torch.bfloat16)
+        out, lse = c.run()
+        if p < 26:
+            c.check(out, lse)
+            continue
+        for i in range(2):
+            kv = [c.c.values(w, i, c.ctx[i])[:, 0] for w in range(2)]
+            for h in range(2):
+                o, _, A, _ = q8_ref.attention(c.q[i, :, h].double(), kv, [c.kt[i, :, 0].double(), c.vt[i, :, 0].double()],
+                                              c.see[i].to(DEV), c.scale)
+                tol = o.abs() * 2.0 ** -8 + A * (2.0 ** -11 + 2.0 ** -20) + 2.0 ** -30   # bf16, P as f16, 1 / l
+                assert ((out[i, :, h].double() - o).abs() <= tol).all(), (p, i, h)
+    for p in range(16, 44):
+        c = Case(n, 2, 1, 128, ctx=(300, 40), seed=p)
+        c.q = c.q * 2.0 ** p
+        out, lse = c.run()
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all(), p
+        v = torch.cat([c.c.values(1, 0, 300), c.c.values(1, 1, 40), c.vt.double().flatten(0, 1)])
+        assert out.abs().max() <= v.abs().max() * (1 + 2.0 ** -8) * (1 + 2.0 ** -10), p
