@@ -59,7 +59,6 @@ constexpr float kHead = 11.f;          // P of a new maximum is 2^11
 // 40 rows 80 us there and 103 us here, 80 rows 83 us and 141 us; 20 x 2736 tokens:
 // 111 us and 75 us, 115 us and 136 us; up to 32 rows are one pass here).
 constexpr long kWideRows = 32;
-constexpr int kTreeTop = 8;            // tree rows as f16: amax in [2^8, 2^9), as large as codes
 
 // D += A (16x16, row) * B (16x8, col), f16 inputs, f32 accumulators.
 __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -77,15 +76,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
-
-// Exponent e with amax (bf16 magnitude bits, finite) * 2^-e in [2^top, 2^(top+1)).
-__device__ __forceinline__ int f16_exponent(uint32_t amax_bits, int top) {
-  return amax_bits < 0x80u ? -126 - top : (int)(amax_bits >> 7) - 127 - top;
-}
-// Two packed bf16 -> two f16 scaled by `inv` (a power of two).
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float inv) {
-  return f32x2_to_f16x2(bf16_lo(w) * inv, bf16_hi(w) * inv);
 }
 
 template <int D, int NR>
@@ -252,7 +242,8 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
 
   // The softmax of a step for row tile nr: scores sc (f32 fragments of NH
   // halves: tokens g, g + 8 of rows 2c, 2c + 1) to the f16 fragments of P^T.
-  // For each half: kmul, what a K product counts for, and ev, the V exponent.
+  // kmul, what a K product counts for, and ev, the V exponent: of each half, or
+  // for one half (tree rows) of each of its two tokens.
   // bits[r]: the tokens that row 2c + r sees, unless it sees all.
   auto softmax = [&](auto nh, int nr, float (*sc)[4], const float* kmul, const float* ev, bool all,
                      const uint32_t* bits, uint32_t (*pt)[2]) {
@@ -260,7 +251,10 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
 #pragma unroll
     for (int h = 0; h < NH; ++h)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sc[h][e] = fmaf(sc[h][e], mul[nr][e & 1] * kmul[h], ev[h]);
+      for (int e = 0; e < 4; ++e) {
+        const int at = NH == 1 ? e >> 1 : h;
+        sc[h][e] = fmaf(sc[h][e], mul[nr][e & 1] * kmul[at], ev[at]);
+      }
     if (!all) {
 #pragma unroll
       for (int h = 0; h < NH; ++h)
@@ -303,10 +297,16 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
       float w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = ex2(sc[h][e] - m[e & 1]);
-      // (a half that is not there has weights 0 and must not meet 2^inf)
-      const float down = ex2(fminf(-ev[h], 126.f));
+      if (NH == 1) {
+        const float down[2] = {ex2(-ev[0]), ex2(-ev[1])};
 #pragma unroll
-      for (int r = 0; r < 2; ++r) l[nr][r] = fmaf(w[r] + w[2 + r], down, l[nr][r]);
+        for (int r = 0; r < 2; ++r) l[nr][r] = fmaf(w[r], down[0], fmaf(w[2 + r], down[1], l[nr][r]));
+      } else {
+        // (a half that is not there has weights 0 and must not meet 2^inf)
+        const float down = ex2(fminf(-ev[h], 126.f));
+#pragma unroll
+        for (int r = 0; r < 2; ++r) l[nr][r] = fmaf(w[r] + w[2 + r], down, l[nr][r]);
+      }
       pt[h][0] = movmatrix(f32x2_to_f16x2(w[0], w[1]));
       pt[h][1] = movmatrix(f32x2_to_f16x2(w[2], w[3]));
     }
@@ -430,14 +430,15 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
     if (lane == 0) raise_status(p.status, DDT_ERR_TIMEOUT);
   }
 
-  // ---- tree steps: the rows' own bf16 K/V, as f16 under a power of two per step
+  // ---- tree steps: the rows' own bf16 K/V, as f16 under a power of two per tree
+  // row, so that no row's size shows in another's (the mask may hide it)
   const int tfirst = first >= nctx ? first : first + (nctx - first + kWarps - 1) / kWarps * kWarps;
   for (int s = tfirst; !idle && s < hi; s += kWarps) {
     const int t0 = (s - nctx) * kHalf;
     const int cnt = min(kHalf, n - t0);
     const uint16_t* kt = p.kt + (((int64_t)b * p.n_max + t0) * p.c.hkv + kvh) * D;
     const uint16_t* vt = p.vt + (((int64_t)b * p.n_max + t0) * p.c.hkv + kvh) * D;
-    uint32_t kmax = 0;
+    uint32_t kmax[2] = {0, 0};  // of tokens g, g + 8
     uint4 kw[2][KH][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -448,12 +449,18 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
           const int t = j * 8 + g;
           uint4 x = make_uint4(0, 0, 0, 0);
           if (t < cnt) x = __ldg((const uint4*)(kt + t * stride + (c * KH + h) * 16) + q);
-          kmax = max_finite_bf16(max_finite_bf16(max_finite_bf16(max_finite_bf16(kmax, x.x), x.y), x.z), x.w);
+          kmax[j] = max_finite_bf16(max_finite_bf16(max_finite_bf16(max_finite_bf16(kmax[j], x.x), x.y), x.z), x.w);
           kw[j][h][q] = x;
         }
-    kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);
-    const int ek = min(max(f16_exponent(kmax, kTreeTop), DDT_Q8_EXP_MIN), DDT_Q8_EXP_MAX);
-    const float kinv = pow2i(-ek);
+    float kmul[2], kinv[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int o = 1; o < 4; o *= 2) kmax[j] = max(kmax[j], __shfl_xor_sync(0xFFFFFFFFu, kmax[j], o));
+      const int ek = tree_exponent(kmax[j]);
+      kmul[j] = pow2i(ek);
+      kinv[j] = pow2i(-ek);
+    }
     float sc[NR][1][4];
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr)
@@ -464,9 +471,10 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const uint4 &x = kw[0][h][w >> 1], &y = kw[1][h][w >> 1];
-        const uint32_t a[4] = {bf16x2_to_f16x2(word(x, (w & 1) * 2), kinv), bf16x2_to_f16x2(word(y, (w & 1) * 2), kinv),
-                               bf16x2_to_f16x2(word(x, (w & 1) * 2 + 1), kinv),
-                               bf16x2_to_f16x2(word(y, (w & 1) * 2 + 1), kinv)};
+        const uint32_t a[4] = {bf16x2_to_f16x2(word(x, (w & 1) * 2), kinv[0]),
+                               bf16x2_to_f16x2(word(y, (w & 1) * 2), kinv[1]),
+                               bf16x2_to_f16x2(word(x, (w & 1) * 2 + 1), kinv[0]),
+                               bf16x2_to_f16x2(word(y, (w & 1) * 2 + 1), kinv[1])};
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
           const uint2 q = q_frag(nr, h * 4 + w);
@@ -475,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
       }
     // V: tokens 2c, 2c+1, 8+2c, 9+2c, elements g*D/8 ..
     uint32_t v[4][D / 16];
-    uint32_t vmax = 0;
+    uint32_t vmax[4] = {0, 0, 0, 0};
     bool odd = false;  // a wild element
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -489,16 +497,22 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
           const uint32_t w = word(x, e);
           odd |= has_wild(w);
           v[i][q * 4 + e] = tame_bf16x2(w);
-          vmax = max(vmax, max_bf16(v[i][q * 4 + e]));
+          vmax[i] = max(vmax[i], max_bf16(v[i][q * 4 + e]));
         }
       }
     }
-    vmax = __reduce_max_sync(0xFFFFFFFFu, vmax);
     odd = __any_sync(0xFFFFFFFFu, odd);
-    const int ev = min(max(f16_exponent(vmax, kTreeTop), DDT_Q8_EXP_MIN), DDT_Q8_EXP_MAX);
-    const float vinv = pow2i(-ev);
+    float vinv[4], ev[2];  // ev: of tokens g, g + 8, from a lane that holds their V
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int o = 4; o < 32; o *= 2) vmax[i] = max(vmax[i], __shfl_xor_sync(0xFFFFFFFFu, vmax[i], o));
+      const int e = tree_exponent(vmax[i]);
+      vinv[i] = pow2i(-e);
+      const float other = (float)__shfl_sync(0xFFFFFFFFu, e, g >> 1);
+      if ((g & 1) == (i & 1)) ev[i >> 1] = other;
+    }
     uint32_t pt[NR][1][2];
-    const float kmul = pow2i(ek), evf = (float)ev;
     const uint32_t cbits = cnt >= kHalf ? 0xFFFFu : (1u << cnt) - 1u;
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
@@ -508,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
         const int j = (q0 + nr * 8 + 2 * c + r) / p.g;
         see[r] = j < n ? (__ldg(p.mask + ((int64_t)b * p.n_max + j) * p.W + (t0 >> 5)) >> (t0 & 31)) & cbits : 0u;
       }
-      softmax(std::integral_constant<int, 1>(), nr, sc[nr], &kmul, &evf, false, see, pt[nr]);
+      softmax(std::integral_constant<int, 1>(), nr, sc[nr], kmul, ev, false, see, pt[nr]);
       if (odd) {
         // a wild V element reaches the rows that see its token, and no others
         for (int t = 0; t < cnt; ++t)
@@ -527,8 +541,8 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
     }
 #pragma unroll
     for (int w = 0; w < NT; ++w) {
-      const uint32_t x0 = bf16x2_to_f16x2(v[0][w], vinv), x1 = bf16x2_to_f16x2(v[1][w], vinv);
-      const uint32_t y0 = bf16x2_to_f16x2(v[2][w], vinv), y1 = bf16x2_to_f16x2(v[3][w], vinv);
+      const uint32_t x0 = bf16x2_to_f16x2(v[0][w], vinv[0]), x1 = bf16x2_to_f16x2(v[1][w], vinv[1]);
+      const uint32_t y0 = bf16x2_to_f16x2(v[2][w], vinv[2]), y1 = bf16x2_to_f16x2(v[3][w], vinv[3]);
       const uint32_t a[4] = {prmt(x0, x1, 0x5410), prmt(x0, x1, 0x7632), prmt(y0, y1, 0x5410),
                              prmt(y0, y1, 0x7632)};
 #pragma unroll

@@ -3,8 +3,9 @@
 //
 // Mathematics: as in attn_q8.cu (codes as f16, K exponents on the scores, V
 // exponents in the softmax's reference, queries f16 under a power of two per
-// row); tree rows become f16 under a power of two per 16 rows.  P is
-// f16 too, so kind::f16 takes both products with f16 operands.
+// row); each tree row becomes f16 under its own powers of two for K and V, which
+// the softmax's reference takes as it takes the blocks'.  P is f16 too, so
+// kind::f16 takes both products with f16 operands.
 //
 // What bounds it: R rows of a kv head want 4 R d flops per context token, so
 // the tensor pipe, and beside it the 2^x of every score (MUFU) and the shared
@@ -48,7 +49,6 @@ constexpr int kSlots = 4;
 constexpr float kSlack = 6.f;                // the reference moves when a score passes it by 2^6
 constexpr float kHead = 9.f;                 // P of a new maximum is 2^9: at most 2^15 in f16
 constexpr float kFar = 1048576.f;            // references from here on have a last place of 2^-3 and more
-constexpr int kTreeTop = 8;                  // tree rows as f16: amax in [2^8, 2^9), as large as codes
 constexpr int kGroup = 16;                   // tokens that share a place and an exponent
 constexpr int kGroups = BN / kGroup;
 constexpr int SN = 64;                       // tokens of a softmax step: half a KV tile
@@ -62,8 +62,9 @@ struct __align__(16) Shared {
   long long wait_cycles;
   uint32_t tmem_base;
   int abort, pick;
-  float2 scales[4][kGroups];  // (what a K product counts for, V exponent)
-  uint32_t amax[2][2][kGroups];  // K, V: largest magnitudes of a tree tile's groups, from two warps each
+  float2 scales[4][kGroups];  // context tile: (what a K product counts for, V exponent) of each group
+  // tree tile: the same of each row, and 2^-(V exponent)
+  __align__(16) float row_k[4][BN], row_v[4][BN], row_d[4][BN];
   uint32_t odd[32];           // tree rows with a wild V element
 };
 
@@ -101,24 +102,6 @@ __device__ __forceinline__ uint32_t desc_lo(const void* at, uint32_t lbo_bytes) 
 __device__ __forceinline__ uint32_t tile_at(int r, int ch) {
   return (uint32_t)((ch >> 3) * kHalfTile + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
 }
-// AND of v over a converter warpgroup's 128 threads (named barrier `id`).
-__device__ __forceinline__ bool all_of_converter(int id, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)v), "r"(id)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float inv) {
-  return f32x2_to_f16x2(bf16_lo(w) * inv, bf16_hi(w) * inv);
-}
-// amax (bf16 magnitude bits, finite) * 2^-e in [2^top, 2^(top+1)).
-__device__ __forceinline__ int f16_exponent(uint32_t amax_bits, int top) {
-  return amax_bits < 0x80u ? -126 - top : (int)(amax_bits >> 7) - 127 - top;
-}
 
 __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8Params p) {
   extern __shared__ unsigned char smem_raw[];
@@ -134,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&sh->kv_full[s], 4);
       mbar_init(&sh->kv_empty[s], 1);
-      mbar_init(&sh->sc_full[s], 2);
+      mbar_init(&sh->sc_full[s], 8);
     }
     for (int t = 0; t < 2; ++t)
       for (int h = 0; h < 2; ++h) {
@@ -243,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
   } else if (wg >= 3) {
     // ------------------------------------------------------------ converters
     static_assert(kRegsConvert == 96, "what the block is launched with");
-    const int kind = wg - 3, bar_id = 1 + 2 * kind;  // K, V
+    const int kind = wg - 3;  // K, V
     const int cw = warp & 3, ct = tid & 127;
     const int tok = ct >> 2, c4 = ct & 3;  // of 32 tokens; 16 elements of a 64-wide slice
     const uint32_t stride = (uint32_t)p.c.hkv * D;
@@ -304,19 +287,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     }
     for (int i = 0; go && i < nctx; ++i) {
       const int e = __shfl_sync(0xFFFFFFFFu, now.e, (i & 3) * 8 + (lane & 7));
-      if (cw == 0) {
+      if (cw == 0 && lane < kGroups) {
         // what a K code counts for; the V exponent
-        if (lane < kGroups) {
-          if (kind == 0)
-            sh->scales[i & 3][lane].x = e == kMissing ? 1.f : q8_scale(e);
-          else
-            sh->scales[i & 3][lane].y = e == kMissing ? -INFINITY
-                                                      : e == DDT_Q8_EXP_NAN ? __int_as_float(0x7FC00000)
-                                                                            : (float)q8_exp(e);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->sc_full[i & 3]);
+        if (kind == 0)
+          sh->scales[i & 3][lane].x = e == kMissing ? 1.f : q8_scale(e);
+        else
+          sh->scales[i & 3][lane].y = e == kMissing ? -INFINITY
+                                                    : e == DDT_Q8_EXP_NAN ? __int_as_float(0x7FC00000)
+                                                                          : (float)q8_exp(e);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->sc_full[i & 3]);
       if ((i & 3) == 1) then = look_up((i & ~3) + 4);
       if ((i & 3) == 3) now = then;  // from here on for tile i + 1
       go = slot_free(i);
@@ -332,15 +313,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
       }
       done(i);
     }
-    for (int i = nctx; i < ntiles; ++i) {
-      // ---- a tile of tree rows: bf16 to f16 under a power of two per group
+    for (int i = nctx; go && i < ntiles; ++i) {
+      // ---- a tile of tree rows: bf16 to f16 under a power of two per row, so that
+      // no row's size shows in another's (the mask may hide it)
       const int row0 = (t_lo + i - nct) * BN;
       const uint16_t* src = (kind ? p.vt : p.kt) + (((int64_t)b * p.n_max + row0) * p.c.hkv + kvh) * D + c4 * 16;
       unsigned char* dst = sKV + slot_of(i) * kTile;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {  // 64 rows
-        go = all_of_converter(bar_id, go);  // (the four warps leave together; amax may be written again)
-        if (!go) break;
         uint4 w[4][2];  // pass q as for the codes
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -351,9 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
             if (row0 + r < n) w[q][h] = __ldg((const uint4*)(src + (int64_t)r * stride + (q & 1) * 64) + h);
           }
         }
-        // largest finite magnitudes, a group from two warps
+        float inv[2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < 2; ++q) {  // a row: four lanes, two slices
           uint32_t m = 0;
           bool odd = false;
 #pragma unroll
@@ -365,43 +345,42 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
             }
             m = max_finite_bf16(max_finite_bf16(max_finite_bf16(max_finite_bf16(m, v.x), v.y), v.z), v.w);
           }
-          const int tr = row0 + half * 64 + q * 32 + tok;
-          if (odd) atomicOr(&sh->odd[tr >> 5], 1u << (tr & 31));
-          m = __reduce_max_sync(0xFFFFFFFFu, m);
-          if (lane == 0) sh->amax[kind][cw & 1][half * 4 + 2 * q + (cw >> 1)] = m;
-        }
-        asm volatile("bar.sync %0, 128;" ::"r"(bar_id) : "memory");
-        const int gl = half * 4 + (lane & 3);
-        const uint32_t m = max(sh->amax[kind][0][gl], sh->amax[kind][1][gl]);
-        const int e = min(max(f16_exponent(m, kTreeTop), DDT_Q8_EXP_MIN), DDT_Q8_EXP_MAX);
-        if (cw == 0) {
-          if (lane < 4) {
-            if (kind == 0)
-              sh->scales[i & 3][gl].x = pow2i(e);
-            else
-              sh->scales[i & 3][gl].y = (float)e;
+          const int r = half * 64 + q * 32 + tok;
+          if (odd) atomicOr(&sh->odd[(row0 + r) >> 5], 1u << ((row0 + r) & 31));
+          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          const int e = tree_exponent(m);
+          inv[q] = pow2i(-e);
+          if (c4 == 0) {
+            if (kind == 0) {
+              sh->row_k[i & 3][r] = pow2i(e);
+            } else {
+              sh->row_v[i & 3][r] = (float)e;
+              sh->row_d[i & 3][r] = inv[q];
+            }
           }
-          __syncwarp();
-          if (half && lane == 0) mbar_arrive(&sh->sc_full[i & 3]);
         }
-        if (half == 0) go = slot_free(i);
-        if (!go) continue;
+        if (half) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->sc_full[i & 3]);
+        } else {
+          go = slot_free(i);
+          if (!go) break;
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float inv = pow2i(-__shfl_sync(0xFFFFFFFFu, e, (q >> 1) * 2 + (cw >> 1)));
           uint4 f[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t u[4] = {w[q][h].x, w[q][h].y, w[q][h].z, w[q][h].w};
 #pragma unroll
-            for (int z = 0; z < 4; ++z) u[z] = bf16x2_to_f16x2(u[z], inv);
+            for (int z = 0; z < 4; ++z) u[z] = bf16x2_to_f16x2(u[z], inv[q >> 1]);
             f[h] = make_uint4(u[0], u[1], u[2], u[3]);
           }
           store(dst, half * 64 + (q >> 1) * 32 + tok, q & 1, f[0], f[1]);
         }
-        if (half) done(i);
       }
-      if (!go) break;
+      if (go) done(i);
     }
     asm volatile("bar.arrive 2, 512;" ::: "memory");
   } else {
@@ -451,30 +430,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_col = lane_base + kColS + 128 * t, o_col = lane_base + kColO + 128 * t;
     const uint32_t* mrow = p.mask + ((int64_t)b * p.n_max + (row_valid ? jq : 0)) * p.W;
-    for (int j = 0; tile_live && j < 2 * ntiles; ++j) {
+    // the scores of step j are there
+    auto scores_of = [&](int j) {
       const int i = j >> 1, half = j & 1;
-      const bool tree = t_lo + i >= nct;
-      const int base = (t_lo + i - (tree ? nct : 0)) * BN + half * SN;
-      const int cnt = min(SN, (tree ? n : T) - base);
-      ok = __all_sync(0xFFFFFFFFu, (half || wait(&sh->sc_full[i & 3], (uint32_t)(i >> 2) & 1u, sh)) &&
-                                       wait(&sh->s_full[t][half], (uint32_t)i & 1u, sh));
+      const bool there = __all_sync(0xFFFFFFFFu, (half || wait(&sh->sc_full[i & 3], (uint32_t)(i >> 2) & 1u, sh)) &&
+                                                     wait(&sh->s_full[t][half], (uint32_t)i & 1u, sh));
+      if (there) fence_after();
+      return there;
+    };
+    // the reference, and with it l, for a step whose largest t is `top`: what O has to be multiplied by
+    auto refer = [&](float top, bool& move) {
+      float alpha = 1.f;
+      move = top - m_ref > kSlack + kHead;
+      if (move) {
+        const float to = reference_below(top, kHead, kSlack);
+        alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - to);
+        m_ref = to;
+        l *= alpha;
+      }
+      return alpha;
+    };
+    // P of step j is written: O under the reference, then the product may begin
+    auto hand_over = [&](int j, float alpha, bool move) {
+      const int half = j & 1;
+      if (j > 0 && __any_sync(0xFFFFFFFFu, move)) {
+        // PV_t(j - 1) is complete behind the next commit on the other half's S
+        if (!__all_sync(0xFFFFFFFFu, wait(&sh->s_full[t][half ^ 1], (uint32_t)((j + 1) >> 1) & 1u, sh))) return false;
+        fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_col + 32 * c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st32(o_col + 32 * c, o);
+        }
+      }
+      tmem_st_wait();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->p_full[t][half]);
+      return true;
+    };
+
+    const int ctx_steps = 2 * min(max(nct - t_lo, 0), ntiles);
+    for (int j = 0; tile_live && j < ctx_steps; ++j) {
+      const int i = j >> 1, half = j & 1;
+      const int cnt = min(SN, T - (t_lo + i) * BN - half * SN);
+      ok = scores_of(j);
       if (!ok) break;
-      fence_after();
       const float2* scale = &sh->scales[i & 3][half * (SN / kGroup)];
       uint32_t r[SN];
 #pragma unroll
       for (int c = 0; c < SN / 32; ++c) tmem_ld32(s_col + half * SN + 32 * c, r + 32 * c);
       tmem_ld_wait();
-      if (tree || cnt < SN) {
+      if (cnt < SN) {
 #pragma unroll
-        for (int w = 0; w < SN / 32; ++w) {
-          const int have = cnt - 32 * w;
-          uint32_t bits = have >= 32 ? 0xFFFFFFFFu : (have > 0 ? (1u << have) - 1u : 0u);
-          if (tree) bits = row_valid && (base >> 5) + w < p.W ? bits & __ldg(mrow + (base >> 5) + w) : 0u;
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!((bits >> e) & 1u)) r[32 * w + e] = 0xFF800000u;  // -inf
-        }
+        for (int e = 0; e < SN; ++e)
+          if (e >= cnt) r[e] = 0xFF800000u;  // -inf
       }
       // t = f s + V exponent; its largest from the largest s of each group (f > 0)
       float f[SN / kGroup], ev[SN / kGroup], top = -INFINITY;
@@ -490,14 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
           m2[(e >> 1) & 1] = fmax3(m2[(e >> 1) & 1], __uint_as_float(r[q * 16 + e]), __uint_as_float(r[q * 16 + e + 1]));
         top = fmaxf(top, fmaf(fmaxf(m2[0], m2[1]), f[q], ev[q]));
       }
-      float alpha = 1.f;
-      const bool move = top - m_ref > kSlack + kHead;
-      if (move) {
-        const float to = reference_below(top, kHead, kSlack);
-        alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - to);
-        m_ref = to;
-        l *= alpha;
-      }
+      bool move;
+      const float alpha = refer(top, move);
       const float m = m_ref == -INFINITY ? 0.f : m_ref;
       float c_of[SN / kGroup];  // P = 2^(f s + c)
 #pragma unroll
@@ -541,25 +549,78 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
         }
         tmem_st16(s_col + half * SN + 16 * c, pk);
       }
-      if (j > 0 && __any_sync(0xFFFFFFFFu, move)) {
-        // PV_t(j - 1) is complete behind the next commit on the other half's S
-        ok = __all_sync(0xFFFFFFFFu, wait(&sh->s_full[t][half ^ 1], (uint32_t)((j + 1) >> 1) & 1u, sh));
-        if (!ok) break;
-        fence_after();
+      ok = hand_over(j, alpha, move);
+      if (!ok) break;
+    }
+    // Tree rows: scales by the row, masks by the bit.  Few steps of many, so in two
+    // passes over 32 scores at a time, which leaves the context's steps their
+    // registers (8 trees of 257 rows over 8192 tokens: 614 us, 596 us with a scale
+    // per 16 rows, 757 us with the rows' scales in the body of every step).
+    for (int j = ctx_steps; tile_live && ok && j < 2 * ntiles; ++j) {
+      const int i = j >> 1, half = j & 1;
+      const int base = (t_lo + i - nct) * BN + half * SN;
+      ok = scores_of(j);
+      if (!ok) break;
+      // t of row base + e, -inf where the mask hides it, back over its score
+      float top = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(o_col + 32 * c, o);
-          tmem_ld_wait();
+      for (int c = 0; c < SN / 32; ++c) {
+        const int have = n - base - 32 * c;
+        if (have <= 0) break;
+        uint32_t bits = row_valid ? __ldg(mrow + (base >> 5) + c) : 0u;
+        if (have < 32) bits &= (1u << have) - 1u;
+        const float4* k4 = (const float4*)&sh->row_k[i & 3][half * SN + 32 * c];
+        const float4* v4 = (const float4*)&sh->row_v[i & 3][half * SN + 32 * c];
+        uint32_t r[32];
+        tmem_ld32(s_col + half * SN + 32 * c, r);
+        tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st32(o_col + 32 * c, o);
+        for (int e = 0; e < 32; e += 4) {
+          const float k[4] = {k4[e / 4].x, k4[e / 4].y, k4[e / 4].z, k4[e / 4].w};
+          const float v[4] = {v4[e / 4].x, v4[e / 4].y, v4[e / 4].z, v4[e / 4].w};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {  // (FLT_MIN: all that a smaller factor multiplies is nothing)
+            const float x = fmaf(__uint_as_float(r[e + z]), fmaxf(mul * k[z], FLT_MIN), v[z]);
+            r[e + z] = (bits >> (e + z)) & 1u ? __float_as_uint(x) : 0xFF800000u;
+          }
+          top = fmax3(top, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+          top = fmax3(top, __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
         }
+        tmem_st32(s_col + half * SN + 32 * c, r);
       }
       tmem_st_wait();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->p_full[t][half]);
+      bool move;
+      const float alpha = refer(top, move);
+      const float m = m_ref == -INFINITY ? 0.f : m_ref;
+#pragma unroll 1
+      for (int c = 0; c < SN / 32; ++c) {
+        const float4* d4 = (const float4*)&sh->row_d[i & 3][half * SN + 32 * c];
+        uint32_t r[32], pk[16];
+        if (n - base - 32 * c <= 0) {  // no rows: no weights
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = 0u;
+          tmem_st16(s_col + half * SN + 16 * c, pk);
+          continue;
+        }
+        tmem_ld32(s_col + half * SN + 32 * c, r);
+        tmem_ld_wait();
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float d[4] = {d4[e / 4].x, d4[e / 4].y, d4[e / 4].z, d4[e / 4].w};
+          float w[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            w[z] = ex2(__uint_as_float(r[e + z]) - m);
+            sum[z] = fmaf(w[z], d[z], sum[z]);
+          }
+          pk[e / 2] = f32x2_to_f16x2(w[0], w[1]);
+          pk[e / 2 + 1] = f32x2_to_f16x2(w[2], w[3]);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st16(s_col + half * SN + 16 * c, pk);
+      }
+      ok = hand_over(j, alpha, move);
     }
     if (tile_live && ok && ntiles > 0) ok = __all_sync(0xFFFFFFFFu, wait(&sh->o_full, 0, sh));
     asm volatile("bar.sync 2, 512;" ::: "memory");  // the converter's marks in sh->odd are complete

@@ -132,6 +132,19 @@ __device__ __forceinline__ uint32_t max_finite_bf16(uint32_t m, uint32_t w) {
 }
 
 
+// Exponent e with amax (bf16 magnitude bits, finite) * 2^-e in [2^top, 2^(top+1)).
+__device__ __forceinline__ int f16_exponent(uint32_t amax_bits, int top) {
+  return amax_bits < 0x80u ? -126 - top : (int)(amax_bits >> 7) - 127 - top;
+}
+// Exponent of a tree row as f16: its amax in [2^8, 2^9), as large as codes.
+__device__ __forceinline__ int tree_exponent(uint32_t amax_bits) {
+  return q8_exp(f16_exponent(amax_bits, 8));
+}
+// Two packed bf16 -> two f16 scaled by `inv` (a power of two).
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float inv) {
+  return f32x2_to_f16x2(bf16_lo(w) * inv, bf16_hi(w) * inv);
+}
+
 // Tree V values from 2^57 on, infinities and NaN are no operands of the
 // products, where even a weight of 0 would make NaN of them: they count as 0
 // there, and as infinities (or NaN) in the rows whose mask shows them.

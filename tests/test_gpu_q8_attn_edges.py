@@ -1,7 +1,7 @@
 """Tree attention over the 8-bit cache where its surroundings are hostile:
 pages that are not there beside pages of NaN codes, caches that end inside a
-tile with NaN codes around them, tree rows out of all proportion, scores of any size.  Reference and
-tolerance are those of test_gpu_q8_attn."""
+tile with NaN codes around them, tree rows out of all proportion, scores of any
+size.  Reference and tolerance are those of test_gpu_q8_attn."""
 import pytest
 import torch
 
@@ -86,6 +86,57 @@ def test_huge_tree_values_reach_only_those_who_see_them(n, d):
     huge = c.vt.abs() >= 2.0 ** 57
     c.vt = torch.where(huge, c.vt * float("inf"), c.vt)
     c.check(out, lse)
+
+
+@pytest.mark.parametrize("n,d", [(2, 128), (9, 64), (9, 128), (70, 128), (140, 128)])
+def test_a_tree_row_does_not_show_where_it_is_not_seen(n, d):
+    """Rows of every magnitude that a bf16 row can have, in the middle of the
+    others: those that do not see them keep their results to the bit, and those
+    results are right."""
+    c = Case(n, 4, 2, d, ctx=(50, 0), seed=n)
+    hidden = [1] if n < 9 else [3, 7, n - 2]
+    c.see[:, :, hidden] = False
+    c.kt[:, hidden], c.vt[:, hidden] = 0.0, 0.0
+    out, lse = c.run()
+    c.check(out, lse)                 # (also the hidden rows' own results: their queries see others)
+    for size in (2.0 ** -60, 1.0, 2.0 ** 20, 2.0 ** 40, 2.0 ** 56, 2.0 ** 57, 1e30, 3e38, float("inf"), float("nan")):
+        c.kt[:, hidden], c.vt[:, hidden] = size, -size
+        again = c.run()
+        assert torch.equal(out.view(torch.int16), again[0].view(torch.int16)), size
+        assert torch.equal(lse, again[1]), size
+
+
+@pytest.mark.parametrize("n,d", [(5, 64), (9, 128), (70, 128), (140, 128)])
+def test_tree_rows_of_unequal_size(n, d):
+    """Rows whose K, and others whose V, are 2^-30 to 2^30 of their neighbours',
+    each seen by rows that do not see the larger ones."""
+    c = Case(n, 4, 1, d, ctx=(0, 33), seed=n, exps=(-9, -9))
+    c.see[:] = False
+    for j in range(n):                # row j sees itself and the rows of its own size below it
+        c.see[:, j, j % 4:j + 1:4] = True
+    size = torch.tensor([1.0, 2.0 ** 30, 2.0 ** -30, 2.0 ** 15], device=DEV)[torch.arange(n, device=DEV) % 4]
+    c.vt = (c.vt * size[None, :, None, None]).to(torch.bfloat16)
+    c.kt = (c.kt * size.flip(0)[None, :, None, None]).to(torch.bfloat16)
+    c.q = (c.q / size.flip(0)[None, :, None, None]).to(torch.bfloat16)
+    c.ctx[1] = 0 if n == 5 else 33
+    out, lse = c.run()
+    full = c.vt
+    for z in range(4):                # the tolerance's max|v| is that of the rows that are seen
+        rows = torch.arange(z, n, 4)
+        c.vt = torch.where((torch.arange(n, device=DEV) % 4 == z)[None, :, None, None], full, 0.0)
+        _check_rows(c, out, lse, rows)
+
+
+def _check_rows(c, out, lse, rows):
+    """Case.check for the given query rows alone."""
+    sub = Case(len(rows), c.q.shape[2], c.c.hkv, c.q.shape[3], ctx=c.ctx, seed=0)
+    n = c.n
+    sub.c, sub.scale, sub.status = c.c, c.scale, c.status
+    sub.q, sub.see = c.q[:, rows].contiguous(), c.see[:, rows][:, :, rows]
+    sub.kt, sub.vt = c.kt[:, rows].contiguous(), c.vt[:, rows].contiguous()
+    assert not c.see[:, rows][:, :, [j for j in range(n) if j not in rows.tolist()]].any()
+    sub.n_nodes = [len(rows)] * len(c.ctx)
+    sub.check(out[:, rows], lse[:, rows])
 
 
 @pytest.mark.parametrize("n", [1, 9, 70, 140])
