@@ -222,6 +222,12 @@ class VerifyRound:
             for name in ("k_cache", "v_cache", "k_exp", "v_exp"):
                 if x.get(name) is None:
                     raise api.DDTError("bind: input %r is missing" % name)
+            here = self.out["status"].device
+            for name in ("ctx_len", "q", "k_tree", "v_tree", "k_cache", "v_cache", "k_exp", "v_exp",
+                         "page_table"):
+                if x.get(name) is not None and x[name].device != here:
+                    raise api.DDTError("bind: %r must be on %s, got a %s tensor"
+                                       % (name, here, x[name].device))
             api._check_rows_q8("bind", x["k_tree"], x["v_tree"], x["k_cache"])
             api._q8_cache("bind", b, x["k_cache"], x["v_cache"], x["k_exp"], x["v_exp"],
                           self.block, pt)
