@@ -5,6 +5,8 @@ size.  Reference and tolerance are those of test_gpu_q8_attn."""
 import pytest
 import torch
 
+from block_draft_tree_b200 import api
+
 import q8_ref
 from test_gpu_q8_attn import Case
 
@@ -176,3 +178,27 @@ def test_scores_of_any_size(n):
         assert torch.isfinite(out).all() and torch.isfinite(lse).all(), p
         v = torch.cat([c.c.values(1, 0, 300), c.c.values(1, 1, 40), c.vt.double().flatten(0, 1)])
         assert out.abs().max() <= v.abs().max() * (1 + 2.0 ** -8) * (1 + 2.0 ** -10), p
+
+
+@pytest.mark.parametrize("page", [0, 48])
+def test_waits_of_the_kernel_for_few_rows_run_out(page):
+    """A batch whose codes take the whole memory bandwidth, so that some of the
+    thousands of waits on copies meet a bound of a few cycles: the status tells
+    (out of ten calls, one has to), and the next call with the default bound
+    gives what the one before gave."""
+    c = Case(1, 32, 8, 128, page=page, ctx=[8160] * 64, seed=page)
+    want = c.run()
+    assert int(c.status) == 0
+    told = []
+    for _ in range(10):
+        api.set_wait_limit(4)
+        try:
+            c.run()
+            torch.cuda.synchronize()
+        finally:
+            api.set_wait_limit(0)
+        told.append(int(c.status))
+        again = c.run()
+        assert int(c.status) == 0
+        assert torch.equal(want[0], again[0]) and torch.equal(want[1], again[1])
+    assert 5 in told and set(told) <= {0, 5}
