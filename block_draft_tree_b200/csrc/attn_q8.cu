@@ -502,13 +502,14 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
       }
     }
     odd = __any_sync(0xFFFFFFFFu, odd);
-    float vinv[4], ev[2];  // ev: of tokens g, g + 8, from a lane that holds their V
+    float ev[2];  // of tokens g, g + 8, from a lane that holds their V
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
       for (int o = 4; o < 32; o *= 2) vmax[i] = max(vmax[i], __shfl_xor_sync(0xFFFFFFFFu, vmax[i], o));
       const int e = tree_exponent(vmax[i]);
-      vinv[i] = pow2i(-e);
+#pragma unroll
+      for (int w = 0; w < D / 16; ++w) v[i][w] = bf16x2_to_f16x2(v[i][w], pow2i(-e));
       const float other = (float)__shfl_sync(0xFFFFFFFFu, e, g >> 1);
       if ((g & 1) == (i & 1)) ev[i >> 1] = other;
     }
@@ -541,10 +542,8 @@ __global__ void __launch_bounds__(kThreads, NR <= 2 ? 3 : 2)
     }
 #pragma unroll
     for (int w = 0; w < NT; ++w) {
-      const uint32_t x0 = bf16x2_to_f16x2(v[0][w], vinv[0]), x1 = bf16x2_to_f16x2(v[1][w], vinv[1]);
-      const uint32_t y0 = bf16x2_to_f16x2(v[2][w], vinv[2]), y1 = bf16x2_to_f16x2(v[3][w], vinv[3]);
-      const uint32_t a[4] = {prmt(x0, x1, 0x5410), prmt(x0, x1, 0x7632), prmt(y0, y1, 0x5410),
-                             prmt(y0, y1, 0x7632)};
+      const uint32_t a[4] = {prmt(v[0][w], v[1][w], 0x5410), prmt(v[0][w], v[1][w], 0x7632),
+                             prmt(v[2][w], v[3][w], 0x5410), prmt(v[2][w], v[3][w], 0x7632)};
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) mma16816(o[nr][w], a, pt[nr][0][0], pt[nr][0][1]);
     }
