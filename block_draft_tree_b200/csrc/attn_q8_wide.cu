@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_wide_kernel(const AttnQ8P
       float c_of[SN / kGroup];  // P = 2^(f s + c)
 #pragma unroll
       for (int q = 0; q < SN / kGroup; ++q) c_of[q] = ev[q] - m;
-      if (__any_sync(0xFFFFFFFFu, fabsf(m) > kFar)) {
+      if (fabsf(m) > kFar) {
         // t rounded first, as its maximum was: in one fma with m, P could pass f16's range
 #pragma unroll
         for (int q = 0; q < SN / kGroup; ++q) {

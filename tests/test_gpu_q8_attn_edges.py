@@ -202,3 +202,17 @@ def test_waits_of_the_kernel_for_few_rows_run_out(page):
         assert int(c.status) == 0
         assert torch.equal(want[0], again[0]) and torch.equal(want[1], again[1])
     assert 5 in told and set(told) <= {0, 5}
+
+
+@pytest.mark.parametrize("n", [9, 70, 140])
+def test_a_row_depends_on_its_own_query_alone(n):
+    """One query of scores beyond any range, one of NaN: the other rows keep
+    their results to the bit."""
+    c = Case(n, 4, 1, 128, ctx=(300, 40), seed=n)
+    out, lse = c.run()
+    c.q[0, 5, 2] *= 2.0 ** 30
+    c.q[1, 2, 0] = float("nan")
+    o2, l2 = c.run()
+    assert torch.isfinite(o2[0, 5, 2]).all() and o2[1, 2, 0].isnan().all()
+    o2[0, 5, 2], l2[0, 5, 2], o2[1, 2, 0], l2[1, 2, 0] = out[0, 5, 2], lse[0, 5, 2], out[1, 2, 0], lse[1, 2, 0]
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
