@@ -28,9 +28,10 @@
 // fragments; for V, lane (g, c) holds tokens 2c, 2c+1, 8+2c, 9+2c and chunk g,
 // whose pairs one byte permute interleaves for the conversion to f16;
 // P^T turns between the products by movmatrix.
-// Measured: one row of 32 ragged sequences of 1024 .. 32768 tokens, 32/8 heads,
-// 64-token pages, 190 us = 5.8 TB/s, 0.88 of the copy rate; 4 x 131072 tokens,
-// 16/1 heads, 37 us with the merge of 111 splits.
+// Tree rows become f16 under a power of two per row, for K and V apart.
+// Measured, calls in turn: one row of 32 ragged sequences of 1024 .. 32768 tokens,
+// 32/8 heads, 64-token pages, 196 .. 210 us in several runs, 0.83 .. 0.89 of the
+// copy rate; 4 x 131072 tokens, 16/1 heads, 35 us with the merge of 111 splits.
 #include <algorithm>
 #include <type_traits>
 
@@ -56,8 +57,10 @@ constexpr int kStep = 2 * kHalf;       // tokens of a step
 constexpr float kSlack = 4.f;          // the reference moves when a score passes it by 2^4
 constexpr float kHead = 11.f;          // P of a new maximum is 2^11
 // Rows per kv head beyond which d = 128 takes the wide kernel (4 x 16384 tokens:
-// 40 rows 80 us there and 103 us here, 80 rows 83 us and 141 us; 20 x 2736 tokens:
-// 111 us and 75 us, 115 us and 136 us; up to 32 rows are one pass here).
+// 40 rows 90 us there and 100 us here, 80 rows 92 us and 137 us; 20 x 2736 tokens:
+// 125 us and 76 us, 125 us and 131 us; up to 32 rows are one pass here).  So trees
+// of few rows more than 32 in a large batch would be better off here; the rule
+// looks at rows alone.
 constexpr long kWideRows = 32;
 
 // D += A (16x16, row) * B (16x8, col), f16 inputs, f32 accumulators.
@@ -724,7 +727,9 @@ struct Plan {
 // The wide kernel's pairs of row tiles and KV splits (steps: tiles of 128
 // tokens): the fewest waves x tiles of a CTA, a split's partials and their
 // merge counted as kMergeTiles tiles (measured on 16 ragged trees of 129 rows:
-// 380 us in three splits, 348 us in one).
+// 418 us in three splits, 380 us in one).  The steps are those of max_ctx: a bound
+// far above the contexts leaves most splits empty (one tree of 65 rows over 4096
+// tokens: 37 us with a bound of 4096, 115 us with 131072).
 Plan plan_wide(const ddt_attn_q8_args* a, long R) {
   constexpr long kMergeTiles = 8;
   Plan pl = {};
@@ -757,8 +762,9 @@ Plan plan_of(const ddt_attn_q8_args* a) {
   const long slots = (long)device_sm_count() * (pl.nr <= 2 ? 3 : 2);
   // as many splits as fill the device, of at least 2 steps a warp; long
   // contexts in splits of at most kLong steps, so that ragged ones even out (32
-  // ragged sequences: 564 us in one split each; 40 to 128 steps are alike, 32
-  // would cut 4 x 131072 tokens into more than one wave: 50 us against 37 us)
+  // ragged sequences: 233 us so, 303 us without; at the step that took it, 40 to
+  // 128 steps were alike, and 32 cut 4 x 131072 tokens into more than one wave: 50
+  // us against 37 us)
   constexpr long kLong = 64;
   long ns = std::max(1L, slots / std::max(1L, base));
   ns = std::min(ns, std::max(1L, steps / (2 * kWarps)));

@@ -35,7 +35,7 @@ __device__ __forceinline__ void attn_q8_lengths(const AttnQ8Params& p, int b, bo
 
 // The (sequence, kv head) group of a block's z index: longest contexts first,
 // so that the last blocks to start are short ones (measured on 16 trees of 129
-// rows over 1024 .. 16384 tokens: 570 us in order, 348 us so).  Batches beyond
+// rows over 1024 .. 16384 tokens: 439 us in order, 380 us so).  Batches beyond
 // kOrdered run in order.
 constexpr int kOrdered = 256;
 __device__ __forceinline__ int group_of(const AttnQ8Params& p, int z, int* s_pick) {

@@ -14,21 +14,25 @@
 //   * warpgroups 3 and 4 convert K and V: codes come from global memory into
 //     registers (the next tile's loads are issued as the last one's registers
 //     are used up), become f16, and go to a ring of two 32 KB slots each in
-//     the 128-byte swizzle that the MMAs read; tree rows likewise.  The codes never pass through a staging buffer, and any
-//     page size works, since no box has to fit a page;
+//     the 128-byte swizzle that the MMAs read; tree rows likewise.  The codes
+//     never pass through a staging buffer, and any page size works, since no
+//     box has to fit a page; what is not in the context is not read;
 //   * warp 1 issues the MMAs by steps of 64 tokens, PV_A(j), QK_A(j+2), PV_B(j),
 //     QK_B(j+2): a tile's scores have two buffers, so the softmax of step j + 1
 //     runs while the products around step j do;
 //   * warpgroups 1 and 2 are the softmax of A and B, a row per thread: the 64
 //     scores in registers, the context bound and the ancestor bitset as masks,
-//     P over the scores' columns, O rescaled only when the reference moves.
+//     P over the scores' columns, O rescaled only when the reference moves; tree
+//     rows, with scales and mask bits of their own, in a second loop.
 // Registers go to where they are needed by setmaxnreg: 40 + 2 x 120 + 2 x 96.
 // KV splits write (O, m, l) partials that attn_q8_combine merges.  Every wait
 // is bounded; one that gives up raises DDT_ERR_TIMEOUT.
-// Measured: 8 trees of 257 rows over 8192 tokens, 64/8 heads, 556 us = 0.79
-// PFLOP/s, half of cuBLAS's bf16 rate (the bf16 kernel for the same shape: 635
-// us); 16 ragged trees of 129 rows in 64-token pages 346 us.  The MMAs are busy
-// two thirds of a step, MUFU and the issue slots half of it each.
+// Measured, one call behind a flush of L2 / back to back for 2 s: 8 trees of 257
+// rows over 8192 tokens, 64/8 heads, 623 / 576 us = 0.71 / 0.77 PFLOP/s, under
+// half of cuBLAS's bf16 rate (the bf16 kernel over the same context: 526 / 516
+// us); 16 ragged trees of 129 rows 393 / 354 us (bf16: 469 / 450 us).  Under the
+// power cap, in longer runs, up to 670 us and 435 us.  The MMAs are busy two
+// thirds of a step, MUFU and the issue slots half of it each.
 #include <cfloat>
 
 #include "attn_q8.cuh"

@@ -15,9 +15,9 @@
 // stored: each input byte is read once and each code written once, which is
 // what bounds a prompt (3 bytes per element); a single token is a launch's
 // latency.  Measured: 4 prompts of up to 8192 tokens, 8 heads of 128, written
-// and read back in 63 us (0.85 of the copy rate), 8 contexts of up to 32768
-// tokens read in 211 us (the copy rate); both were bound by their issue slots
-// (80 us, 232 us) until magnitudes and multiplies went two at a time.
+// and read back in 61 us (0.87 of the copy rate), 8 contexts of up to 32768
+// tokens read in 209 .. 219 us (0.96 .. 1.0 of it); both were bound by their
+// issue slots (80 us, 232 us) until magnitudes and multiplies went two at a time.
 #include "launch.h"
 #include "q8_common.cuh"
 
@@ -358,8 +358,10 @@ ddt_status launch_kv_read_q8(const ddt_kv_read_q8_args* a, cudaStream_t stream) 
   p.v_out = (uint4*)a->v_out;
   p.n_max = a->n_max;
   p.status = a->dev_status;
-  // 32 rows a CTA where that still gives every SM several (8 contexts of up to
-  // 32768 tokens: 244 us, 254 us with 16), 8 where the call is small
+  // 32 rows a CTA where that still gives every SM several (32 contexts of up to
+  // 8192 tokens, 2 heads of 128: 80 us, 123 us with 16 and 209 us with 8 rows; 8
+  // contexts of up to 32768 tokens, 8 heads: 219, 209 and 281 us), 8 where the
+  // call is small
   const int64_t ctas = (int64_t)((a->n_max + kReadRows - 1) / kReadRows) * a->batch * 2;
   p.rows = ctas >= 8 * device_sm_count() ? kReadRows : kReadRows / 4;
   const dim3 grid((a->n_max + p.rows - 1) / p.rows, a->batch, 2);

@@ -54,9 +54,9 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) 
 
 // Two e4m3 codes (low byte first) -> two f16, exactly: e4m3 is a subset of f16,
 // and its NaN code stays NaN.  (The same by integers, a byte permute, a shift
-// and a mask for each pair, takes more issue slots than the conversion costs:
-// 575 us against 554 us for 8 trees of 257 rows over 8192 tokens, 216 us against
-// 211 us for 32 ragged decoding steps.)
+// and a mask for each pair, takes more issue slots than the conversion costs: at
+// the step that took it, 575 us against 554 us for 8 trees of 257 rows over 8192
+// tokens, 216 us against 211 us for 32 ragged decoding steps.)
 __device__ __forceinline__ uint32_t codes_to_f16(uint16_t c) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));

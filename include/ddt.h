@@ -597,8 +597,9 @@ ddt_status ddt_kv_commit_q8(const ddt_kv_commit_q8_args* a, cudaStream_t stream)
  * rows: k_out / v_out [batch][n_max][hkv][d], exactly the values that the
  * cache stands for.  Rows at or past ctx_len[b] are written as 0.  first may
  * be NULL (0 everywhere).  A position below ctx_len[b] that is outside the
- * cache, or a negative first[b], reads as 0 and raises DDT_ERR_INVALID_ARG in
- * dev_status.  Output pointers 16-byte aligned. */
+ * cache reads as 0 and raises DDT_ERR_INVALID_ARG in dev_status; so does a
+ * negative first[b], for its positions below 0.  Output pointers 16-byte
+ * aligned. */
 typedef struct ddt_kv_read_q8_args {
   ddt_q8_cache cache;
   const int32_t* ctx_len;
@@ -617,9 +618,11 @@ ddt_status ddt_kv_read_q8(const ddt_kv_read_q8_args* a, cudaStream_t stream);
  * with mask bit 0 set is an ordinary decoding step.  Scores, softmax sums and
  * outputs accumulate in fp32; queries, codes and softmax weights meet the
  * tensor cores as f16 under power-of-two scales (codes exactly, a query
- * element to 2^-39 of its row's largest, a weight to 2^-11).  Tree K/V rows
- * hold magnitudes up to 2^56; larger ones may count as infinities.  A
- * non-finite tree value reaches only the rows whose mask shows it.  A page id
+ * element to 2^-39 of its row's largest, a weight to 2^-11; what a token adds to
+ * the output below 2^-32 of the largest |value| of any block or tree row that the
+ * row attends to may be lost).  Tree K/V rows hold magnitudes up to 2^56; larger
+ * ones may count as infinities.  Each row has scales of its own: neither its size
+ * nor a non-finite value shows in rows whose mask hides it.  A page id
  * outside the pool below ctx_len raises DDT_ERR_INVALID_ARG in dev_status and
  * its tokens are left out.
  * The workspace (its size may be 0) needs no initial contents and holds
